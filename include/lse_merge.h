@@ -259,6 +259,117 @@ int lse_merge_decode_attention_ws(const void* q, const void* k, const void* v,
                                   lse_merge_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * An 8-bit KV cache: quantised as it is written, read back, and attended over
+ * (for one query token per sequence, or for a tree of drafted ones).
+ *
+ * The cache holds e4m3 codes and one fp32 scale per token and KV head, for
+ * keys and for values:
+ *   k_cache, v_cache [B, Hkv, L, D] (1 byte per element): element (b,h,l,d) at
+ *                    b*k_b + h*k_h + l*k_l + d, value code * k_scale(b,h,l)
+ *   k_scale, v_scale [B, Hkv, L] fp32: element (b,h,l) at b*ks_b + h*ks_h + l*ks_l
+ *
+ * lse_merge_kv_quantize writes T tokens per sequence.  Token j of sequence b
+ * (j < T, and j < count[b] where count is given) goes to position start[b] + j;
+ * a token whose position is outside [0, L) is not written, nor is any other
+ * row of the cache.  Its row x[D] is k(b,h,i,:) (and v(b,h,i,:)) with i = j, or
+ * i = select[b*T + j] where select is given (the accepted drafts of a tree, in
+ * order; an index outside [0, S) is not written).  Per row:
+ *     a     = max over the finite x[d] of |x[d]|
+ *     scale = 2^e, e the smallest integer >= -126 with a <= 448 * 2^e
+ *             (1 when a = 0)
+ *     code  = x[d] / scale rounded to the nearest e4m3 (ties to even); an
+ *             element that is not finite is stored as NaN
+ * A power of two keeps the division exact, so that values read back and
+ * written again stay what they are.
+ *
+ * lse_merge_kv_dequantize reads them back: row j < T of sequence b of k and v
+ * is code * scale of position start[b] + j, rounded once to dtype; rows with
+ * j >= count[b] or a position outside [0, L) are zeros.
+ *
+ *   k, v     [B, Hkv, S, D] of dtype (S = T without select, and in dequantize):
+ *            element (b,h,i,d) at b*x_b + h*x_h + i*x_t + d; written by dequantize
+ *   start    int32 [B]; count int32 [B] or NULL; select int32 [B, T] or NULL
+ *            (NULL in dequantize); device pointers
+ *   D        64 or 128; caches, k and v 16-byte aligned with strides of whole
+ *            16-byte multiples; positions of what is written are distinct
+ *            (no stride may map two elements to one address)
+ *   dtype    quantize: any lse_merge_dtype; dequantize: any
+ * The scales may have any strides >= 0 (quantize: distinct positions).  One
+ * kernel launch.  Returns the codes of lse_merge; LSE_MERGE_EUNSUP for another D.
+ */
+#define LSE_MERGE_E4M3 3   /* a cache's element type; not one of lse_merge_dtype */
+
+typedef struct {
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    void *k, *v;                       /* read by quantize, written by dequantize */
+    const int32_t *start, *count, *select;
+    int64_t k_b, k_h, k_l, v_b, v_h, v_l;          /* caches */
+    int64_t ks_b, ks_h, ks_l, vs_b, vs_h, vs_l;    /* scales */
+    int64_t kx_b, kx_h, kx_t, vx_b, vx_h, vx_t;    /* k and v */
+    int32_t B, Hkv, L, D, T, S, dtype, reserved;
+} lse_merge_kv_args;
+
+int lse_merge_kv_quantize(const lse_merge_kv_args* args, lse_merge_stream_t stream);
+int lse_merge_kv_dequantize(const lse_merge_kv_args* args, lse_merge_stream_t stream);
+
+/* Attention of T query tokens per sequence over a cache, and over the T tokens
+ * themselves, which are not in the cache yet (a tree of drafted tokens).
+ * Query (b,t,h) attends, over KV head h / (Hq / Hkv), to
+ *   - the cached keys [0, len_b), len_b = kv_len[b] clamped to [0, L] (L when
+ *     kv_len is NULL), and
+ *   - the drafted keys j < n_b for which bit j of tree[b*tree_b + t] is set,
+ *     n_b = draft_len[b] clamped to [0, T] (T when draft_len is NULL):
+ *     s_j = scale * <q, k_j>,  lse = log sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j
+ * Rows t >= n_b, and rows that see no key, give 0 and -inf.  Keys that a row
+ * does not see never reach it (NaN there does not leak).  Without drafts
+ * (k_draft NULL; then tree and v_draft are not read) the T queries attend to the
+ * cache alone; T = 1 is then a decode step.
+ *
+ *   q            [B, T, Hq, D] of dtype; k_draft, v_draft [B, Hkv, T, D] of dtype
+ *   k, v         the cache [B, Hkv, L, D], of dtype (cache_dtype == dtype) or
+ *                LSE_MERGE_E4M3 with k_scale and v_scale [B, Hkv, L], positive
+ *   tree         int64 [B, T] (row stride tree_b; 0 = the same tree for all)
+ *   out_o        dense [B, T, Hq, D] of out_dtype; out_lse dense [B, T, Hq] fp32
+ *   dtype        LSE_MERGE_BF16 or LSE_MERGE_F16;  1 <= T <= 64;  D 64 or 128;
+ *                Hq a multiple of Hkv with Hq / Hkv <= 16
+ *   R            shards the cache is cut into (ceil(len_b / R) keys each);
+ *                partials of the shards are merged by weight
+ *   workspace    lse_merge_tree_workspace_bytes() bytes (0: may be NULL),
+ *                16-byte aligned, no initial content needed; calls that may run
+ *                at the same time need workspaces of their own
+ *   q, k, v, the drafts and out_o are 16-byte aligned, with strides of whole 16-byte
+ *   multiples; scale strides are any >= 0; a tree word is 8-byte aligned
+ * One launch, or two where partials are merged.  Returns the codes of
+ * lse_merge; LSE_MERGE_EUNSUP for a D, T, group size or dtype outside the above.
+ */
+#define LSE_MERGE_TREE_MAX_T 64
+
+typedef struct {
+    const void *q, *k, *v;
+    const float *k_scale, *v_scale;
+    const void *k_draft, *v_draft;
+    const int64_t* tree;
+    const int32_t *kv_len, *draft_len;
+    void* out_o;
+    float* out_lse;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t q_b, q_t, q_h;
+    int64_t k_b, k_h, k_l, v_b, v_h, v_l;
+    int64_t ks_b, ks_h, ks_l, vs_b, vs_h, vs_l;
+    int64_t kd_b, kd_h, kd_t, vd_b, vd_h, vd_t;
+    int64_t tree_b;
+    int32_t B, T, Hq, Hkv, L, D, R, dtype, cache_dtype, out_dtype;
+    float scale;
+    int32_t reserved;
+} lse_merge_tree_args;
+
+/* Bytes of the workspace: the partials of R shards (and of the drafts), fp32. */
+int lse_merge_tree_workspace_bytes(int B, int T, int Hq, int D, int R, int drafts, int64_t* bytes);
+int lse_merge_tree_attention(const lse_merge_tree_args* args, lse_merge_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Context-parallel exchange and merge in one kernel.
  *
  * The step before the merge on the CP-decode page (section "코드 분석 / 1.

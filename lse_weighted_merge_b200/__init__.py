@@ -20,7 +20,8 @@ _API = ("merge", "merge_state_", "merge_host", "release_host_workspace", "merge_
         "state_update_raw", "decode_attention", "decode_raw", "plan_query", "strerror", "LseMergeError", "dtype_code",
         "F32", "F16", "BF16", "PATH_AUTO", "PATH_VECTOR", "PATH_LATENCY", "PATH_SCALAR",
         "PATH_STREAM")
-__all__ = list(_API) + list(_CP)
+_KV = ("kv_quantize_", "kv_dequantize", "decode_attention_fp8", "tree_attention", "tree_mask")
+__all__ = list(_API) + list(_CP) + list(_KV)
 
 
 def __getattr__(name):
@@ -30,4 +31,8 @@ def __getattr__(name):
     if name in _CP:
         from . import cp
         return getattr(cp, name)
+    if name in _KV:
+        from . import kv_cache
+        value = globals()[name] = getattr(kv_cache, name)   # found directly from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

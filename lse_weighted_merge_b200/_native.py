@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "liblse_merge.so")
@@ -29,6 +30,8 @@ CP_IPC_HANDLE_BYTES = 64
 CP_FLAG_CROSS_GPU_PROTOCOL = 1
 CP_FLAG_TEST_SILENT_LAST_RANK = 2
 CP_NOALLOC_SCRATCH_BYTES = 16 << 20
+E4M3 = 3            # element type of an 8-bit cache
+TREE_MAX_T = 64
 
 # Every symbol include/lse_merge.h declares.
 EXPORTS = ("lse_merge", "lse_merge_with_path", "lse_merge_plan_query", "lse_merge_state_update",
@@ -40,7 +43,8 @@ EXPORTS = ("lse_merge", "lse_merge_with_path", "lse_merge_plan_query", "lse_merg
            "lse_merge_cp_exchange_merge_noalloc", "lse_merge_cp_noalloc_status",
            "lse_merge_decode_workspace_bytes", "lse_merge_decode_attention_ws",
            "lse_merge_host_stage_bytes", "lse_merge_host_create", "lse_merge_host_destroy",
-           "lse_merge_host")
+           "lse_merge_host", "lse_merge_kv_quantize", "lse_merge_kv_dequantize",
+           "lse_merge_tree_workspace_bytes", "lse_merge_tree_attention")
 ABI_VERSION = 4
 
 
@@ -95,6 +99,12 @@ def cp_args(world: int, rank_begin: int, local_o, local_lse, out_o, out_lse, ws,
     return CpArgs(int(world), int(rank_begin), len(local_o), arr(local_o), arr(local_lse),
                   arr(out_o), arr(out_lse), arr(ws), int(B), int(H), int(D),
                   int(in_dtype), int(out_dtype), int(timeout_ns), int(flags))
+
+
+# lse_merge_kv_args and lse_merge_tree_args, field by field in their order (a
+# packed bytes object costs a fraction of filling a ctypes structure).
+KV_ARGS = struct.Struct("=9Q18q8i")
+TREE_ARGS = struct.Struct("=13Q23q10ifi")
 
 
 class LseMergeError(RuntimeError):
@@ -168,6 +178,11 @@ def _load() -> ctypes.CDLL:
     lib.lse_merge_cp_ipc_open.restype = i
     lib.lse_merge_cp_ipc_close.argtypes = [vp]
     lib.lse_merge_cp_ipc_close.restype = i
+    for f in (lib.lse_merge_kv_quantize, lib.lse_merge_kv_dequantize, lib.lse_merge_tree_attention):
+        f.argtypes = [ctypes.c_char_p, vp]
+        f.restype = i
+    lib.lse_merge_tree_workspace_bytes.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int64)]
+    lib.lse_merge_tree_workspace_bytes.restype = i
     if lib.lse_merge_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH}: ABI version {lib.lse_merge_version()} != {ABI_VERSION}")
     return lib
@@ -284,6 +299,37 @@ def decode_raw(q_ptr: int, k_ptr: int, v_ptr: int, kv_len_ptr: int, B: int, Hq: 
     else:
         rc = lib.lse_merge_decode_partials(*args, out_ptr, out_lse_ptr, stream or None)
     return _check(rc, check)
+
+
+def kv_quantize_raw(fields, stream: int = 0, check: bool = True) -> int:
+    """lse_merge_kv_quantize; ``fields`` are those of lse_merge_kv_args in order."""
+    args = KV_ARGS.pack(*fields)
+    rc = _fast.kv_quantize(args, stream or 0) if _fast is not None else lib.lse_merge_kv_quantize(args, stream or None)
+    return _check(rc, check)
+
+
+def kv_dequantize_raw(fields, stream: int = 0, check: bool = True) -> int:
+    """lse_merge_kv_dequantize; ``fields`` are those of lse_merge_kv_args in order."""
+    args = KV_ARGS.pack(*fields)
+    rc = (_fast.kv_dequantize(args, stream or 0) if _fast is not None
+          else lib.lse_merge_kv_dequantize(args, stream or None))
+    return _check(rc, check)
+
+
+def tree_raw(fields, stream: int = 0, check: bool = True) -> int:
+    """lse_merge_tree_attention; ``fields`` are those of lse_merge_tree_args in order."""
+    args = TREE_ARGS.pack(*fields)
+    rc = (_fast.tree_attention(args, stream or 0) if _fast is not None
+          else lib.lse_merge_tree_attention(args, stream or None))
+    return _check(rc, check)
+
+
+def tree_workspace_bytes(B: int, T: int, Hq: int, D: int, R: int, drafts: bool) -> int:
+    n = ctypes.c_int64(0)
+    rc = lib.lse_merge_tree_workspace_bytes(B, T, Hq, D, R, 1 if drafts else 0, ctypes.byref(n))
+    if rc != OK:
+        _raise(rc)
+    return n.value
 
 
 def host_stage_bytes(R: int, B: int, H: int, D: int, in_dtype: int, out_dtype: int) -> int:

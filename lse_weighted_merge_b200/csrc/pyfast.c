@@ -18,12 +18,17 @@
  *   cp_exchange_merge(args_address, stream) -> int
  *                                      lse_merge_cp_exchange_merge on an
  *                                      lse_merge_cp_args the caller owns
+ *   kv_quantize(args, stream), kv_dequantize(args, stream),
+ *   tree_attention(args, stream) -> int
+ *                                      the calls of those names; args is a bytes
+ *                                      object that holds the argument struct
  * Pointers and the stream are integers (0 for NULL / the legacy stream).  The
  * return value is the library's code; nothing raises on a library error.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "lse_merge.h"
 
@@ -134,6 +139,51 @@ static PyObject* fast_cp(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return PyLong_FromLong(rc);
 }
 
+/* The struct in a bytes object of exactly its size (copied: it is aligned). */
+static int as_struct(PyObject* o, void* dst, Py_ssize_t size) {
+    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != size) {
+        PyErr_Format(PyExc_TypeError, "the arguments must be a bytes object of %zd bytes", size);
+        return -1;
+    }
+    memcpy(dst, PyBytes_AS_STRING(o), (size_t)size);
+    return 0;
+}
+
+static PyObject* fast_kv(PyObject* const* a, Py_ssize_t n, const char* name,
+                         int (*call)(const lse_merge_kv_args*, lse_merge_stream_t)) {
+    lse_merge_kv_args args;
+    void* stream;
+    if (!nargs_ok(n, 2, name) || as_struct(a[0], &args, sizeof args) || as_ptr(a[1], &stream)) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(&args, (lse_merge_stream_t)stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* fast_kv_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    return fast_kv(a, n, "kv_quantize", lse_merge_kv_quantize);
+}
+
+static PyObject* fast_kv_dequantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    return fast_kv(a, n, "kv_dequantize", lse_merge_kv_dequantize);
+}
+
+static PyObject* fast_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    lse_merge_tree_args args;
+    void* stream;
+    if (!nargs_ok(n, 2, "tree_attention") || as_struct(a[0], &args, sizeof args) || as_ptr(a[1], &stream))
+        return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = lse_merge_tree_attention(&args, (lse_merge_stream_t)stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyMethodDef fast_methods[] = {
     {"merge", (PyCFunction)(void (*)(void))fast_merge, METH_FASTCALL,
      "lse_merge_with_path(o, lse, R, B, H, D, strides, in_dtype, out_dtype, out, out_lse, stream, path)"},
@@ -141,6 +191,12 @@ static PyMethodDef fast_methods[] = {
      "lse_merge_state_update(acc, lse_acc, new, lse_new, B, H, D, strides, acc_dtype, new_dtype, stream)"},
     {"cp_exchange_merge", (PyCFunction)(void (*)(void))fast_cp, METH_FASTCALL,
      "lse_merge_cp_exchange_merge(args_address, stream)"},
+    {"kv_quantize", (PyCFunction)(void (*)(void))fast_kv_quantize, METH_FASTCALL,
+     "lse_merge_kv_quantize(args, stream)"},
+    {"kv_dequantize", (PyCFunction)(void (*)(void))fast_kv_dequantize, METH_FASTCALL,
+     "lse_merge_kv_dequantize(args, stream)"},
+    {"tree_attention", (PyCFunction)(void (*)(void))fast_tree, METH_FASTCALL,
+     "lse_merge_tree_attention(args, stream)"},
     {NULL, NULL, 0, NULL},
 };
 
