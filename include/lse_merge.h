@@ -369,6 +369,9 @@ typedef struct {
 int lse_merge_tree_workspace_bytes(int B, int T, int Hq, int D, int R, int drafts, int64_t* bytes);
 int lse_merge_tree_attention(const lse_merge_tree_args* args, lse_merge_stream_t stream);
 
+/* The R that suits these sizes on a GPU of `sms` SMs (1 for sizes out of range). */
+int lse_merge_tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms);
+
 /* ---------------------------------------------------------------------------
  * Context-parallel exchange and merge in one kernel.
  *

@@ -44,7 +44,8 @@ EXPORTS = ("lse_merge", "lse_merge_with_path", "lse_merge_plan_query", "lse_merg
            "lse_merge_decode_workspace_bytes", "lse_merge_decode_attention_ws",
            "lse_merge_host_stage_bytes", "lse_merge_host_create", "lse_merge_host_destroy",
            "lse_merge_host", "lse_merge_kv_quantize", "lse_merge_kv_dequantize",
-           "lse_merge_tree_workspace_bytes", "lse_merge_tree_attention")
+           "lse_merge_tree_workspace_bytes", "lse_merge_tree_attention",
+           "lse_merge_tree_default_splits")
 ABI_VERSION = 4
 
 
@@ -183,6 +184,8 @@ def _load() -> ctypes.CDLL:
         f.restype = i
     lib.lse_merge_tree_workspace_bytes.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int64)]
     lib.lse_merge_tree_workspace_bytes.restype = i
+    lib.lse_merge_tree_default_splits.argtypes = [i] * 7
+    lib.lse_merge_tree_default_splits.restype = i
     if lib.lse_merge_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH}: ABI version {lib.lse_merge_version()} != {ABI_VERSION}")
     return lib

@@ -1,5 +1,7 @@
 """Build the C-ABI shared library (liblse_merge.so) in-tree with nvcc for sm_100a,
-and the small CPython extension (_fast) that forwards its per-call entry points.
+the small CPython extension (_fast) that forwards its per-call entry points, and
+the extension (_torch_ops) that makes the cache's and attention's calls on torch
+tensors.
 
     python -m lse_weighted_merge_b200.build [--verbose]
 """
@@ -60,6 +62,33 @@ def build_fast(lib: str = LIB) -> str:
     return out
 
 
+TORCH_SRC = os.path.join(CSRC, "torch_ops.cpp")
+
+
+def torch_path() -> str:
+    """In-tree path of the extension that takes torch tensors."""
+    import sysconfig
+    return os.path.join(PKG, "_torch_ops" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_torch_ops(lib: str = LIB) -> str:
+    """Compile torch_ops.cpp (g++, the headers of the torch that is installed)
+    against liblse_merge.so, found at run time next to the extension; torch's own
+    libraries are loaded by `import torch` before it."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    out = torch_path()
+    cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", TORCH_SRC,
+           "-L", os.path.dirname(lib), "-l:" + os.path.basename(lib), "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-o", out]
+    subprocess.run(cmd, check=True)
+    return out
+
+
 def build(out: str = LIB, verbose: bool = False, extra: list[str] | None = None) -> str:
     cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", out]
     if verbose:
@@ -69,6 +98,7 @@ def build(out: str = LIB, verbose: bool = False, extra: list[str] | None = None)
     subprocess.run(cmd, check=True)
     if out == LIB:
         build_fast(out)
+        build_torch_ops(out)
     return out
 
 
@@ -76,3 +106,4 @@ if __name__ == "__main__":
     build(verbose="--verbose" in sys.argv)
     print(LIB)
     print(fast_path())
+    print(torch_path())

@@ -468,6 +468,16 @@ int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* pl
     return LSE_MERGE_OK;
 }
 
+// Shards of the cached keys: enough for about two CTAs per SM, a power of two
+// of at least 64 keys each, at most 64.
+int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms) {
+    if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || L < 1 || D < 1 || sms < 1) return 1;
+    const int64_t units = (int64_t)B * Hkv * (((int64_t)T * (Hq / Hkv) + 15) / 16);
+    int R = 1;
+    while (units * R < 2 * (int64_t)sms && R < 64 && R * 64 < L) R *= 2;
+    return R;
+}
+
 int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan) {
     const int e = elem_bytes(a.dtype), ob = elem_bytes(a.out_dtype);
     const bool fp8 = a.cache_dtype == LSE_MERGE_E4M3, drafts = a.k_draft != nullptr;
@@ -678,6 +688,10 @@ int lse_merge_tree_workspace_bytes(int B, int T, int Hq, int D, int R, int draft
     const int rc = lsem::tree_workspace(B, T, Hq, D, R, drafts != 0, &p);
     if (rc == LSE_MERGE_OK) *bytes = p.ws_bytes;
     return rc;
+}
+
+int lse_merge_tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms) {
+    return lsem::tree_default_splits(B, T, Hq, Hkv, L, D, sms);
 }
 
 int lse_merge_plan_query(const void* partial_o, const float* partial_lse, int R, int B, int H,

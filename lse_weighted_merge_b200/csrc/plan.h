@@ -176,6 +176,7 @@ struct TreePlan {
 };
 int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* plan);
 int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan);
+int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms);
 
 // Validate the arguments of lse_merge_state_update and fill *plan.
 int make_state_plan(const void* o_acc, const float* lse_acc, const void* o_new,
