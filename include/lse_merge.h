@@ -372,6 +372,11 @@ int lse_merge_tree_attention(const lse_merge_tree_args* args, lse_merge_stream_t
 /* The R that suits these sizes on a GPU of `sms` SMs (1 for sizes out of range). */
 int lse_merge_tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms);
 
+/* How many blocks of tree attention calls on the current device gave up a wait
+ * between their own warps (never, in working order; their rows are NaN), as of
+ * the work that is complete.  Synchronises. */
+int lse_merge_tree_status(uint32_t* gave_up);
+
 /* ---------------------------------------------------------------------------
  * Context-parallel exchange and merge in one kernel.
  *

@@ -45,7 +45,7 @@ EXPORTS = ("lse_merge", "lse_merge_with_path", "lse_merge_plan_query", "lse_merg
            "lse_merge_host_stage_bytes", "lse_merge_host_create", "lse_merge_host_destroy",
            "lse_merge_host", "lse_merge_kv_quantize", "lse_merge_kv_dequantize",
            "lse_merge_tree_workspace_bytes", "lse_merge_tree_attention",
-           "lse_merge_tree_default_splits")
+           "lse_merge_tree_default_splits", "lse_merge_tree_status")
 ABI_VERSION = 4
 
 
@@ -186,6 +186,8 @@ def _load() -> ctypes.CDLL:
     lib.lse_merge_tree_workspace_bytes.restype = i
     lib.lse_merge_tree_default_splits.argtypes = [i] * 7
     lib.lse_merge_tree_default_splits.restype = i
+    lib.lse_merge_tree_status.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
+    lib.lse_merge_tree_status.restype = i
     if lib.lse_merge_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH}: ABI version {lib.lse_merge_version()} != {ABI_VERSION}")
     return lib

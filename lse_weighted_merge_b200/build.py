@@ -19,9 +19,11 @@ LIB = os.path.join(PKG, "liblse_merge.so")
 SOURCES = [os.path.join(CSRC, "plan.cpp"), os.path.join(CSRC, "lse_merge.cu"),
            os.path.join(CSRC, "decode_attention.cu"), os.path.join(CSRC, "cp_exchange.cu"),
            os.path.join(CSRC, "kv_cache.cu"), os.path.join(CSRC, "tree_attention.cu"),
+           os.path.join(CSRC, "tree_wide.cu"),
            os.path.join(CSRC, "host_pipeline.cpp")]
 HEADERS = [os.path.join(INCLUDE, "lse_merge.h"), os.path.join(CSRC, "plan.h"),
-           os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_common.cuh")]
+           os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_common.cuh"),
+           os.path.join(CSRC, "tree_common.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

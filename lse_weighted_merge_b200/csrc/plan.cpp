@@ -468,12 +468,24 @@ int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* pl
     return LSE_MERGE_OK;
 }
 
-// Shards of the cached keys: enough for about two CTAs per SM, a power of two
-// of at least 64 keys each, at most 64.
+// Shards of the cached keys.  Up to 16 query rows per KV head (rows16 kernel): enough
+// for about two CTAs per SM, a power of two of at least 64 keys each, at most 64.
+// More rows (wide kernel, one CTA per SM, tiles of 128 keys): the R that gives the
+// fewest tiles per SM, with 3 tiles' time for the start and end of a CTA.
 int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms) {
     if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || L < 1 || D < 1 || sms < 1) return 1;
-    const int64_t units = (int64_t)B * Hkv * (((int64_t)T * (Hq / Hkv) + 15) / 16);
+    const int64_t rows = (int64_t)T * (Hq / Hkv);
     int R = 1;
+    if (rows > 16) {
+        const int64_t units = (int64_t)B * Hkv * ((rows + 255) / 256), tiles = ((int64_t)L + 127) / 128;
+        int64_t best = -1;
+        for (int r = 1; r <= 64 && r <= tiles; ++r) {
+            const int64_t cost = (units * r + sms - 1) / sms * ((tiles + r - 1) / r + 3);
+            if (best < 0 || cost < best) best = cost, R = r;
+        }
+        return R;
+    }
+    const int64_t units = (int64_t)B * Hkv;
     while (units * R < 2 * (int64_t)sms && R < 64 && R * 64 < L) R *= 2;
     return R;
 }

@@ -40,67 +40,14 @@
 #include "attn_common.cuh"
 #include "lse_merge.h"
 #include "plan.h"
+#include "tree_common.cuh"
 
 namespace lsem {
 namespace attn {
 namespace {
 
-struct TreeParams {
-    const char *q, *k, *v, *kd, *vd;
-    const float *ks, *vs;
-    const int64_t* tree;
-    const int32_t *kv_len, *draft_len;
-    int64_t q_b, q_t, q_h;                          // byte strides
-    int64_t k_b, k_h, k_l, v_b, v_h, v_l;
-    int64_t kd_b, kd_h, kd_t, vd_b, vd_h, vd_t;
-    int64_t ks_b, ks_h, ks_l, vs_b, vs_h, vs_l;     // element strides
-    int64_t tree_b;
-    int T, Hq, G, L, R, shards, row_tiles;
-    float scale_log2;   // scale * log2(e)
-    float* po;          // partials [B, T, Hq, shards, D], or NULL:
-    float* pl;          // [B, T, Hq, shards]
-    char* out;          // the result [B, T, Hq, D]
-    float* out_lse;     // [B, T, Hq]
-};
-
 constexpr int kRowWarps = 4;
 constexpr int kRowStages = 3;
-
-// Longest key index of a row: nothing beyond it is read.
-struct Shard {
-    int b, hk, r, lo, hi, live;   // live: drafts of the sequence (rows t >= live are dead)
-    bool drafts;
-    const char *kb, *vb;
-};
-
-__device__ __forceinline__ Shard shard_of(const TreeParams& p, int r, int hk, int b) {
-    Shard x;
-    x.b = b;
-    x.hk = hk;
-    x.r = r;
-    x.live = p.draft_len ? min(max(p.draft_len[b], 0), p.T) : p.T;
-    x.drafts = r == p.R;
-    if (x.drafts) {
-        x.lo = 0;
-        x.hi = x.live;
-        x.kb = p.kd + b * p.kd_b + hk * p.kd_h;
-        x.vb = p.vd + b * p.vd_b + hk * p.vd_h;
-    } else {
-        const int len = p.kv_len ? min(max(p.kv_len[b], 0), p.L) : p.L;
-        const int per = (int)(((int64_t)len + p.R - 1) / p.R);
-        x.lo = (int)min((int64_t)len, (int64_t)r * per);
-        x.hi = (int)min((int64_t)len, (int64_t)x.lo + per);
-        x.kb = p.k + b * p.k_b + hk * p.k_h;
-        x.vb = p.v + b * p.v_b + hk * p.v_h;
-    }
-    return x;
-}
-
-// The address of query row `row` of (b, hk).
-__device__ __forceinline__ const char* q_row(const TreeParams& p, int b, int hk, int row) {
-    const int t = row / p.G;
-    return p.q + b * p.q_b + t * p.q_t + (int64_t)(hk * p.G + row - t * p.G) * p.q_h;
-}
 
 // The running state of a warp's online softmax: rows g and g + 8, log2 units.
 template <int D>
@@ -198,18 +145,6 @@ struct Tiles16 {
         }
     }
 
-    // Whether any element of the 16-byte chunk is an infinity or NaN; those become 0.
-    __device__ static bool scrub(uint32_t (&c)[4]) {
-        constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if ((c[i] & kExp) == kExp) c[i] &= 0xffff0000u, bad = true;
-            if ((c[i] >> 16 & kExp) == kExp) c[i] &= 0x0000ffffu, bad = true;
-        }
-        return bad;
-    }
-
     // words: the draft masks of rows g and g + 8 (all ones over a cache).
     __device__ static void attend(const TreeParams& p, const Shard& x, unsigned char* st_p, uint32_t st,
                                   const Query& q, int key0, uint64_t word0, uint64_t word1, int lane,
@@ -256,7 +191,7 @@ struct Tiles16 {
                 uint4* at = reinterpret_cast<uint4*>(st_p + kVOff + c * 16);
                 const uint4 u = *at;
                 uint32_t e[4] = {u.x, u.y, u.z, u.w};
-                if (scrub(e)) {
+                if (scrub16<T>(e)) {
                     *at = make_uint4(e[0], e[1], e[2], e[3]);
                     bad = true;
                 }
@@ -295,31 +230,6 @@ struct Tiles16 {
 };
 
 // -------------------------------------------------------------- e4m3 tiles
-
-// Two e4m3 codes (in the low or high half of c) as two f16.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {
-    uint32_t h;
-    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(c));
-    return h;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t c) {
-    uint32_t h;
-    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(h) : "r"(c));
-    return h;
-}
-// 4-byte global -> shared copy; `bytes` = 0 writes zeros without reading.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// The power of two at or below x (of its bits): 2^floor(log2 x), x > 0.
-__device__ __forceinline__ float pow2_below(float x) {
-    return __uint_as_float(min(max(__float_as_uint(x) & 0x7f800000u, 0x00800000u), 0x7e800000u));
-}
-// 1 / r of a power of two in [2^-126, 2^126].
-__device__ __forceinline__ float pow2_inverse(float r) {
-    return __uint_as_float(0x7f000000u - __float_as_uint(r));
-}
 
 // Tiles of 32 keys: K codes, V codes, K scales, V scales.
 template <typename T, int D>
@@ -573,11 +483,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) tree_rows16_kernel(const TreeP
     using Draft = Tiles16<T, D>;
     constexpr int kRing = kRowStages * (Cache::kBytes > Draft::kBytes ? Cache::kBytes : Draft::kBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - r * p.row_tiles) * 16;
+    const int i = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - i * p.row_tiles) * 16;
     const int rows = p.T * p.G;
     pdl_wait();
     pdl_release();
-    Shard x = shard_of(p, r, blockIdx.y, blockIdx.z);
+    Shard x = shard_of(p, p.r0 + i, blockIdx.y, blockIdx.z);
     if (row0 >= x.live * p.G) x.hi = x.lo;   // dead rows only
     RowState<D> w;
     unsigned char* ring = smem + warp * kRing;
@@ -725,7 +635,6 @@ TreeKernel pick_tree(int D, bool fp8, int out_dtype) {
     return fp8 ? pick_out<T, 128, true>(out_dtype) : pick_out<T, 128, false>(out_dtype);
 }
 
-// cudaFuncSetAttribute once per (kernel, device).
 std::mutex g_tree_mu;
 struct TreeAttr {
     const void* fn;
@@ -734,17 +643,21 @@ struct TreeAttr {
 TreeAttr g_tree_done[256];
 int g_tree_n = 0;
 
-cudaError_t allow_smem(const TreeKernel& k) {
+}  // namespace
+
+cudaError_t allow_smem(const void* fn, int bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(g_tree_mu);
     for (int i = 0; i < g_tree_n; ++i)
-        if (g_tree_done[i].fn == (const void*)k.fn && g_tree_done[i].dev == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-    if (e == cudaSuccess && g_tree_n < 256) g_tree_done[g_tree_n++] = TreeAttr{(const void*)k.fn, dev};
+        if (g_tree_done[i].fn == fn && g_tree_done[i].dev == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && g_tree_n < 256) g_tree_done[g_tree_n++] = TreeAttr{fn, dev};
     return e;
 }
+
+namespace {
 
 int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
     if (!args) return LSE_MERGE_ENULL;
@@ -776,18 +689,21 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
         p.tree_b = a.tree_b;
     }
     p.T = a.T, p.Hq = a.Hq, p.G = pl.G, p.L = a.L, p.R = a.R;
-    p.shards = pl.shards;
+    // More than 16 rows take the wide kernel.  The drafts of a 16-bit cache are
+    // then with its last shard; those of an 8-bit one, whose products are of
+    // another type, stay a shard of the rows16 kernel.
+    const bool wide = pl.rows > 16;
+    p.fold = wide && !fp8 && drafts;
+    p.shards = p.fold ? a.R : pl.shards;
     p.row_tiles = (pl.rows + 15) / 16;
     p.scale_log2 = a.scale * kLog2e;
-    if (pl.shards > 1) {
+    if (p.shards > 1) {
         p.po = static_cast<float*>(a.workspace);
         p.pl = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + pl.ws_l_off);
     } else {
         p.out = static_cast<char*>(a.out_o);
         p.out_lse = a.out_lse;
     }
-    const TreeKernel k = a.dtype == LSE_MERGE_F16 ? pick_tree<__half>(a.D, fp8, a.out_dtype)
-                                                  : pick_tree<__nv_bfloat16>(a.D, fp8, a.out_dtype);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -795,19 +711,27 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = kPdl ? 1 : 0;
-    cudaError_t e = allow_smem(k);
-    if (e == cudaSuccess) {
-        cfg.gridDim = dim3((unsigned)(p.row_tiles * pl.shards), (unsigned)a.Hkv, (unsigned)a.B);
-        cfg.blockDim = dim3(kRowWarps * 32);
-        cfg.dynamicSmemBytes = (size_t)k.smem;
-        e = cudaLaunchKernelEx(&cfg, k.fn, p);
+    cudaError_t e = cudaSuccess;
+    if (!wide || (fp8 && drafts)) {
+        p.r0 = wide ? a.R : 0;
+        const TreeKernel k = a.dtype == LSE_MERGE_F16 ? pick_tree<__half>(a.D, fp8, a.out_dtype)
+                                                      : pick_tree<__nv_bfloat16>(a.D, fp8, a.out_dtype);
+        e = allow_smem((const void*)k.fn, k.smem);
+        if (e == cudaSuccess) {
+            cfg.gridDim = dim3((unsigned)(p.row_tiles * (p.shards - p.r0)), (unsigned)a.Hkv, (unsigned)a.B);
+            cfg.blockDim = dim3(kRowWarps * 32);
+            cfg.dynamicSmemBytes = (size_t)k.smem;
+            e = cudaLaunchKernelEx(&cfg, k.fn, p);
+        }
     }
-    if (e == cudaSuccess && pl.shards > 1) {
+    if (e == cudaSuccess && wide)
+        e = launch_tree_wide(p, a.dtype, fp8, a.out_dtype, a.B, a.Hkv, a.D, kPdl != 0, stream);
+    if (e == cudaSuccess && p.shards > 1) {
         const uint32_t rows = (uint32_t)a.B * a.T * a.Hq, per = 128u / (uint32_t)(a.D / 4);
         cfg.gridDim = dim3((rows + per - 1) / per);
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, pick_merge(a.out_dtype, a.D), (const float*)p.po, (const float*)p.pl, pl.shards,
+        e = cudaLaunchKernelEx(&cfg, pick_merge(a.out_dtype, a.D), (const float*)p.po, (const float*)p.pl, p.shards,
                                rows, static_cast<char*>(a.out_o), a.out_lse);
     }
     if (e != cudaSuccess) {
