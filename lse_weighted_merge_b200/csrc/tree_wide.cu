@@ -9,7 +9,8 @@
 //   * up to 128 rows: both streams have the same rows, stream s the key tiles
 //     s, s + 2, ...; their states are merged at the end, in shared memory.
 // Warps 0-3 and 4-7 are the softmax of stream 0 and 1 (thread = query row = TMEM
-// lane), warps 8-11 bring the tiles, warp 12 issues the products:
+// lane; one thread of each also issues the stream's products), warps 8-11 bring
+// the tiles:
 //   S = Q K^T   128 x 128, Q and K in shared memory (K-major, 128-byte swizzle)
 //   O += P V    128 x D, P in TMEM over S (16 bits, half its columns), V in shared
 //               memory as it lies in the cache (its D is the fast index: MN-major)
@@ -46,7 +47,7 @@ namespace lsem {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 12 * 32;
 constexpr int kTK = 128;                    // keys per tile
 constexpr uint64_t kGiveUpNs = 2000000000;  // longest wait for another warp
 
@@ -98,26 +99,32 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void tm_ld32(uint32_t at, float (&r)[32]) {
-    uint32_t u[32];
+#define LSEM_OP32(c, u) \
+    c(u[0]), c(u[1]), c(u[2]), c(u[3]), c(u[4]), c(u[5]), c(u[6]), c(u[7]), c(u[8]), c(u[9]), c(u[10]), c(u[11]), \
+        c(u[12]), c(u[13]), c(u[14]), c(u[15]), c(u[16]), c(u[17]), c(u[18]), c(u[19]), c(u[20]), c(u[21]), c(u[22]), \
+        c(u[23]), c(u[24]), c(u[25]), c(u[26]), c(u[27]), c(u[28]), c(u[29]), c(u[30]), c(u[31])
+// 32 columns of the thread's lane; the values are there after tm_wait32.
+__device__ __forceinline__ void tm_get32(uint32_t at, float (&f)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : LSEM_OP32("=f", f)
         : "r"(at)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
 }
-__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&u)[16]) {
+// (the operands keep every use of the values behind it)
+__device__ __forceinline__ void tm_wait32(float (&f)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : LSEM_OP32("+f", f)::"memory");
+}
+__device__ __forceinline__ void tm_ld32(uint32_t at, float (&f)[32]) {
+    tm_get32(at, f);
+    tm_wait32(f);
+}
+__device__ __forceinline__ void tm_put32(uint32_t at, const float (&f)[32]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(at)
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        LSEM_OP32("f", f)
         : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -158,7 +165,7 @@ struct Lay {
 };
 
 // Barriers, 8 bytes each, at the control block.
-enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 15, kOFull = 17, kFin = 19, kBars = 20 };
+enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 15, kOFull = 17, kBars = 19 };
 
 struct Ctrl {
     uint64_t bar[kBars];
@@ -323,41 +330,15 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         }
         cp_commit();
     };
-    auto scale_at = [&](int i) -> float {   // of key tid of item i
-        if (i >= items) return 0.f;
-        int j;
-        bool value;
-        item_of(i, pl.n, j, value);
+    const float* ksrc = p.ks + x.b * p.ks_b + x.hk * p.ks_h;
+    const float* vsrc = p.vs + x.b * p.vs_b + x.hk * p.vs_h;
+    auto scale_at = [&](const float* src, int64_t stride, int j) -> float {   // of key tid of tile j
         const int key = x.lo + j * kTK + tid;
-        if (key >= x.hi) return 0.f;
-        return value ? p.vs[x.b * p.vs_b + x.hk * p.vs_h + key * p.vs_l] : p.ks[x.b * p.ks_b + x.hk * p.ks_h + key * p.ks_l];
+        return j < pl.n && key < x.hi ? src[key * stride] : 0.f;
     };
-    for (int i = 0; i < raws; ++i) fetch(i, i);
-    float sc = scale_at(0);
-    int rs = 0;
-    for (int i = 0; i < items; ++i) {
-        int j;
-        bool value;
-        item_of(i, pl.n, j, value);
-        Ring& r = value ? vr : kr;
-        const float scale = sc;
-        sc = scale_at(i + 1);
-        if (pl.two)
-            cp_wait<1>();
-        else
-            cp_wait<2>();
-        wait(bars + 8 * ((value ? kVEmpty : kKEmpty) + r.slot), r.phase, &ctrl->dead);
-        if (value) {
-            const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(scale));
-            if (lane == 0) ctrl->top[j & 1][warp] = __uint_as_float(top);
-            asm volatile("bar.sync 2, 128;" ::: "memory");
-            const float* tp = ctrl->top[j & 1];
-            run = fmaxf(run, pow2_below(fmaxf(fmaxf(tp[0], tp[1]), fmaxf(tp[2], tp[3]))));
-            vs[r.slot * kTK + tid] = scale * pow2_inverse(run);
-            if (tid == 0) ctrl->vref[r.slot] = run;
-        } else {
-            ks[j % nks * kTK + tid] = scale;
-        }
+    int rs = 0, item = 0;
+    // the next item's codes -> f16 in place `r` of its ring
+    auto convert = [&](bool value, Ring& r) {
         unsigned char* tile = smem + (value ? 4 + r.slot : 2 + r.slot) * L::kTile;
         const unsigned char* src = smem + raw(rs);
 #pragma unroll
@@ -376,28 +357,59 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * ((value ? kVFull : kKFull) + r.slot));
         r.next();
-        fetch(i + raws, rs);
+        fetch(item + raws, rs);
+        ++item;
         if (++rs == raws) rs = 0;
+    };
+    auto landed = [&]() {
+        if (pl.two)
+            cp_wait<1>();
+        else
+            cp_wait<2>();
+    };
+    for (int i = 0; i < raws; ++i) fetch(i, i);
+    // the scales come a whole tile ahead
+    float ksc = scale_at(ksrc, p.ks_l, 0), vsc = scale_at(vsrc, p.vs_l, 0);
+    for (int j = -1; j < pl.n; ++j) {
+        if (j + 1 < pl.n) {
+            landed();
+            wait(bars + 8 * (kKEmpty + kr.slot), kr.phase, &ctrl->dead);
+            ks[(j + 1) % nks * kTK + tid] = ksc;
+            ksc = scale_at(ksrc, p.ks_l, j + 2);
+            convert(false, kr);
+        }
+        if (j >= 0) {
+            landed();
+            wait(bars + 8 * (kVEmpty + vr.slot), vr.phase, &ctrl->dead);
+            const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(vsc));
+            if (lane == 0) ctrl->top[j & 1][warp] = __uint_as_float(top);
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+            const float* tp = ctrl->top[j & 1];
+            run = fmaxf(run, pow2_below(fmaxf(fmaxf(tp[0], tp[1]), fmaxf(tp[2], tp[3]))));
+            vs[vr.slot * kTK + tid] = vsc * pow2_inverse(run);
+            if (tid == 0) ctrl->vref[vr.slot] = run;
+            vsc = scale_at(vsrc, p.vs_l, j + 1);
+            convert(true, vr);
+        }
     }
     cp_wait<0>();
 }
 
 // ------------------------------------------------------------ products
 
+// What one thread issues for stream s: S of its tile i, and O += P V of it.
 template <typename TM, int D, bool kFp8>
-__device__ __forceinline__ void issue(const WidePlan& pl, uint32_t smem_u, uint32_t tmem, Ctrl* ctrl, uint32_t bars) {
+struct Products {
     using L = Lay<D>;
-    constexpr uint32_t kIdQK = instr_desc<TM>(kTK, false), kIdPV = instr_desc<TM>(D, true);
-    const int nk = kFp8 || pl.two ? 2 : 3, nv = kFp8 ? 2 : 3;
-    auto slot_phase = [](int j, int n, uint32_t& ph) {
-        ph = (uint32_t)(j / n) & 1u;
-        return j % n;
-    };
-    auto qk = [&](int s, int i) {
-        const int j = pl.tile(s, i);
-        uint32_t ph;
-        const int slot = slot_phase(j, nk, ph);
-        wait(bars + 8 * (kKFull + slot), ph, &ctrl->dead);
+    static constexpr uint32_t kIdQK = instr_desc<TM>(kTK, false), kIdPV = instr_desc<TM>(D, true);
+    const WidePlan& pl;
+    uint32_t smem_u, tmem, bars;
+    Ctrl* ctrl;
+    int s;
+
+    __device__ __forceinline__ void qk(int i) const {
+        const int j = pl.tile(s, i), nk = kFp8 || pl.two ? 2 : 3, slot = j % nk;
+        wait(bars + 8 * (kKFull + slot), (uint32_t)(j / nk) & 1u, &ctrl->dead);
         tc_after();
         const uint32_t q = smem_u + (pl.two ? s : 0) * L::kTile;
         const uint32_t k = smem_u + (slot < 2 ? 2 + slot : 1) * L::kTile;
@@ -406,38 +418,23 @@ __device__ __forceinline__ void issue(const WidePlan& pl, uint32_t smem_u, uint3
             const uint32_t off = (u >> 2) * L::kBlock + (u & 3) * 32;
             mma_ss(tmem + s * kTK, smem_desc(q + off, 16), smem_desc(k + off, 16), kIdQK, u > 0);
         }
-        if (!pl.two || s == 1) tc_commit(bars + 8 * (kKEmpty + slot));
+        tc_commit(bars + 8 * (kKEmpty + slot));
         tc_commit(bars + 8 * (kSFull + s));
-    };
-    auto pv = [&](int s, int i) {
-        const int j = pl.tile(s, i);
-        uint32_t ph;
-        const int slot = slot_phase(j, nv, ph);
-        wait(bars + 8 * (kVFull + slot), ph, &ctrl->dead);
+    }
+    __device__ __forceinline__ void pv(int i) const {
+        const int j = pl.tile(s, i), nv = kFp8 ? 2 : 3, slot = j % nv;
+        wait(bars + 8 * (kVFull + slot), (uint32_t)(j / nv) & 1u, &ctrl->dead);
         wait(bars + 8 * (kPFull + s), (uint32_t)i & 1u, &ctrl->dead);
         tc_after();
         const uint32_t v = smem_u + (4 + slot) * L::kTile;
 #pragma unroll
         for (int u = 0; u < kTK / 16; ++u)
-            mma_ts(tmem + 2 * kTK + s * D, tmem + s * kTK + u * 8, smem_desc(v + u * 2048, L::kBlock), kIdPV, i > 0 || u > 0);
-        if (!pl.two || s == 1) tc_commit(bars + 8 * (kVEmpty + slot));
+            mma_ts(tmem + 2 * kTK + s * D, tmem + s * kTK + u * 8, smem_desc(v + u * 2048, L::kBlock), kIdPV,
+                   i > 0 || u > 0);
+        tc_commit(bars + 8 * (kVEmpty + slot));
         if (i == pl.count(s) - 1) tc_commit(bars + 8 * (kOFull + s));
-    };
-    wait(bars + 8 * kQFull, 0, &ctrl->dead);
-    for (int s = 0; s < 2; ++s)
-        if (pl.count(s) > 0) qk(s, 0);
-    for (int i = 0; i < pl.count(0); ++i)
-        for (int s = 0; s < 2; ++s)
-            if (i < pl.count(s)) {
-                pv(s, i);
-                if (i + 1 < pl.count(s)) qk(s, i + 1);
-            }
-    tc_commit(bars + 8 * kFin);
-    // all that was issued has to be complete before TMEM is freed
-    const uint64_t t0 = global_ns();
-    while (!try_wait(bars + 8 * kFin, 0) && global_ns() - t0 < 2 * kGiveUpNs) {
     }
-}
+};
 
 // ------------------------------------------------------------ queries
 
@@ -479,41 +476,160 @@ __device__ __forceinline__ void load_query(const char* src, unsigned char* tile,
     }
 }
 
+// ------------------------------------------------------------ softmax
+
+// A row's running state: reference (log2 units, kLow .. kHigh below the maximum),
+// sum of weights, and e4m3: the values' scale that O is relative to.
+struct RowSum {
+    float m, l, vref;
+};
+template <typename TM>
+constexpr float kLow = std::is_same<TM, __half>::value ? 7.f : 0.f;
+template <typename TM>
+constexpr float kHigh = std::is_same<TM, __half>::value ? 14.f : 8.f;
+
+// The weights of 32 scores f, their sum and the largest exponent.  kCareful: a
+// mask, and the scaled score rounded before the reference is subtracted (a fused
+// difference of numbers past 2^22 could lie far from that of the rounded ones,
+// which the reference is made from).
+template <typename TM, bool kFp8, bool kCareful>
+__device__ __forceinline__ void weights32(const float (&f)[32], const float4* k4, const float4* v4, uint64_t scale2,
+                                          uint64_t ref2, uint32_t see, uint64_t& sum, float& top, uint32_t* w) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        uint64_t k2[2] = {scale2, scale2};
+        if constexpr (kFp8) {
+            const float4 k = k4[u];
+            k2[0] = pack2f(k.x, k.y), k2[1] = pack2f(k.z, k.w);
+            mul2(k2[0], scale2);
+            mul2(k2[1], scale2);
+        }
+        uint64_t e2[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint64_t a;
+            float e0, e1;
+            if constexpr (kCareful) {
+                a = pack2f(f[4 * u + 2 * h], f[4 * u + 2 * h + 1]);
+                mul2(a, k2[h]);
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(ref2));
+            } else {
+                a = ref2;
+                fma2(a, pack2f(f[4 * u + 2 * h], f[4 * u + 2 * h + 1]), k2[h]);
+            }
+            unpack2f(a, e0, e1);
+            if (kCareful) {
+                e0 = see >> (4 * u + 2 * h) & 1 ? e0 : -INFINITY;
+                e1 = see >> (4 * u + 2 * h + 1) & 1 ? e1 : -INFINITY;
+            }
+            top = fmaxf(top, fmaxf(e0, e1));
+            e2[h] = pack2f(ex2(e0), ex2(e1));
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(e2[h]));
+        }
+        if constexpr (kFp8) {
+            const float4 v = v4[u];
+            mul2(e2[0], pack2f(v.x, v.y));
+            mul2(e2[1], pack2f(v.z, v.w));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float e0, e1;
+            unpack2f(e2[h], e0, e1);
+            w[2 * u + h] = Mma<TM>::pack(e0, e1);
+        }
+    }
+}
+
+// S of one tile (at tS) -> P over it.  The weights are taken relative to the
+// reference that the earlier tiles left, in one pass over S; where the tile's
+// maximum turns out to lie kHigh above it (always in a row's first tile, hardly
+// ever later) the reference moves and the pass is made again.
+template <typename TM, bool kFp8, bool kCareful>
+__device__ __forceinline__ void softmax_pass(uint32_t tS, const float4* k4, const float4* v4, float scale, float ref,
+                                             uint64_t see0, uint64_t see1, float& l, float& top, uint32_t* w) {
+    const uint64_t scale2 = pack2f(scale, scale), ref2 = pack2f(-ref, -ref);
+    uint64_t sum = 0;
+    float fa[32], fb[32];
+    tm_get32(tS, fa);
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        tm_wait32(fa);
+        tm_get32(tS + 32 * c + 32, fb);
+        weights32<TM, kFp8, kCareful>(fa, k4 + 8 * c, v4 + 8 * c, scale2, ref2, (uint32_t)(c ? see1 : see0), sum, top,
+                                      w + 16 * c);
+        tm_wait32(fb);
+        if (c == 0) tm_get32(tS + 64, fa);
+        weights32<TM, kFp8, kCareful>(fb, k4 + 8 * c + 8, v4 + 8 * c + 8, scale2, ref2,
+                                      (uint32_t)((c ? see1 : see0) >> 32), sum, top, w + 16 * c + 16);
+    }
+    float s0, s1;
+    unpack2f(sum, s0, s1);
+    l = s0 + s1;
+}
+
+template <typename TM, int D, bool kFp8>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, const float4* k4, const float4* v4, float vref,
+                                             float scale, bool masked, uint64_t see0, uint64_t see1, bool first,
+                                             RowSum& st) {
+    uint32_t w[kTK / 2];
+    float down = 1.f, l;
+    for (;;) {
+        const float ref = st.m == -INFINITY ? 0.f : st.m;
+        float top = -INFINITY;
+        if (masked || __any_sync(kFull, fabsf(ref) > 4194304.f))
+            softmax_pass<TM, kFp8, true>(tS, k4, v4, scale, ref, see0, see1, l, top, w);
+        else
+            softmax_pass<TM, kFp8, false>(tS, k4, v4, scale, ref, see0, see1, l, top, w);
+        const float next = top + ref - kLow<TM>;
+        const bool move = st.m == -INFINITY ? top != -INFINITY : top > kHigh<TM> && next != st.m;
+        if (!__any_sync(kFull, move)) break;
+        if (move) {
+            down *= ex2(st.m - next);   // 0 at first
+            st.m = next;
+        }
+    }
+    st.l = st.l * down + l;
+    if constexpr (kFp8) {
+        down *= st.vref * pow2_inverse(vref);
+        st.vref = vref;
+    }
+    if (!first && __any_sync(kFull, down != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float f[32];
+            tm_ld32(tO + c, f);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] *= down;
+            tm_put32(tO + c, f);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(w[32 * c + e]);
+        tm_put32(tS + 32 * c, f);
+    }
+    tm_wait_st();
+}
+
 // ------------------------------------------------------------ kernel
 
 template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams p) {
     using L = Lay<D>;
     using TM = typename std::conditional<kFp8, __half, T>::type;
-    constexpr float kLow = std::is_same<TM, __half>::value ? 7.f : 0.f;
-    constexpr float kHigh = std::is_same<TM, __half>::value ? 14.f : 8.f;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem_u = smem_u32(smem);
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + L::kCtrl);
     const uint32_t bars = smem_u + L::kCtrl;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        auto init = [&](int b, int n) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * b), "r"(n) : "memory");
-        };
-        init(kQFull, 8);
-        for (int i = 0; i < 3; ++i) init(kKFull + i, 4), init(kKEmpty + i, 1), init(kVFull + i, 4), init(kVEmpty + i, 1);
-        for (int s = 0; s < 2; ++s) init(kSFull + s, 1), init(kPFull + s, 4), init(kOFull + s, 1);
-        init(kFin, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        ctrl->dead = (smem_u & 1023u) != 0;   // the swizzle's atoms are 1024 bytes
-        ctrl->bad = 0;
-    }
-    if (warp == 12) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctrl->tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    tc_before();
-    __syncthreads();
-    tc_after();
-    const uint32_t tmem = ctrl->tmem;
     pdl_wait();
     pdl_release();
 
@@ -527,17 +643,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     // the scales' rings: keys' by tile, values' by slot
     float* ks = reinterpret_cast<float*>(pl.two ? smem + L::kCtrl + 256 : smem + L::kTile + L::kRaw);
     float* vs = ks + (pl.two ? 3 : 4) * kTK;
+    if (tid == 0) {
+        auto init = [&](int b, int n) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * b), "r"(n) : "memory");
+        };
+        const int users = pl.two ? 2 : 1;   // streams that read a tile
+        init(kQFull, 8);
+        for (int i = 0; i < 3; ++i) {
+            init(kKFull + i, 4), init(kKEmpty + i, users);
+            init(kVFull + i, 4), init(kVEmpty + i, users);
+        }
+        for (int s = 0; s < 2; ++s) init(kSFull + s, 1), init(kPFull + s, 4), init(kOFull + s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        ctrl->dead = (smem_u & 1023u) != 0;   // the swizzle's atoms are 1024 bytes
+        ctrl->bad = 0;
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = ctrl->tmem;
 
     const int s = warp >> 2 & 1;                        // softmax warps: the stream
     const int row = row0 + (pl.two ? 128 * s : 0) + (tid & 127);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's lanes of TMEM
-    float m = -INFINITY, l = 0.f, vref = 1.17549435e-38f;
+    RowSum st{-INFINITY, 0.f, 1.17549435e-38f};
     uint64_t word = 0;
 
-    if (warp == 12) {
-        if (lane == 0) issue<TM, D, kFp8>(pl, smem_u, tmem, ctrl, bars);
-        __syncwarp();
-    } else if (warp >= 8) {
+    if (warp >= 8) {
         if constexpr (kFp8)
             load8<D>(p, x, pl, smem, smem_u, ctrl, bars, ks, vs, tid - 256);
         else
@@ -554,11 +686,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * kQFull);
         const bool idle = row - lane >= last_row;   // no live row in the warp
-        const uint64_t scale2 = pack2f(scale, scale);
         const uint32_t tS = tmem + lanes + s * kTK, tO = tmem + lanes + 2 * kTK + s * D;
+        const Products<TM, D, kFp8> products{pl, smem_u, tmem, bars, ctrl, s};
+        const bool issues = (warp & 3) == 0 && lane == 0;
         const int count = pl.count(s);
         Ring vr{2, pl.two ? 0 : s, 0};
         int kslot = pl.two ? 0 : s;
+        if (issues && count > 0) {
+            wait(bars + 8 * kQFull, 0, &ctrl->dead);
+            products.qk(0);
+        }
+        __syncwarp();
         for (int i = 0; i < count; ++i) {
             const int j = pl.tile(s, i);
             const int nkeys = j < pl.cached ? min(kTK, x.hi - x.lo - j * kTK) : x.live;
@@ -571,112 +709,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             tc_after();
             if (!idle) {
                 const float4* k4 = reinterpret_cast<const float4*>(ks + kslot * kTK);
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kTK / 32; ++c) {
-                    float f[32];
-                    tm_ld32(tS + c * 32, f);
-                    if constexpr (kFp8) {
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float4 k = k4[c * 8 + u];
-                            f[4 * u] *= k.x * scale, f[4 * u + 1] *= k.y * scale;
-                            f[4 * u + 2] *= k.z * scale, f[4 * u + 3] *= k.w * scale;
-                        }
-                    }
-                    if (masked) {
-                        const uint32_t see = (uint32_t)((c < 2 ? see0 : see1) >> (c & 1) * 32);
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) f[u] = see >> u & 1 ? f[u] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int u = 0; u < 32; u += 2) mx = fmaxf(mx, fmaxf(f[u], f[u + 1]));
-                }
-                if (!kFp8 && mx != -INFINITY) mx *= scale;
-                // a new reference where the maximum has left the old one's range
-                float down = 1.f;
-                if (mx - m > kHigh || (m == -INFINITY && mx != -INFINITY)) {
-                    const float ref = mx - kLow;
-                    down = ex2(m - ref);   // 0 at first
-                    m = ref;
-                    l *= down;
-                }
+                const float4* v4 = reinterpret_cast<const float4*>(vs + vr.slot * kTK);
+                float vref = 1.f;
                 if constexpr (kFp8) {
                     wait(bars + 8 * (kVFull + vr.slot), vr.phase, &ctrl->dead);   // the values' scales
-                    const float ref = ctrl->vref[vr.slot];
-                    down *= vref * pow2_inverse(ref);
-                    vref = ref;
+                    vref = ctrl->vref[vr.slot];
+                    __syncwarp();
                 }
-                if (i > 0 && __any_sync(kFull, down != 1.f)) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float f[32];
-                        tm_ld32(tO + c * 32, f);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t u[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(f[16 * h + e] * down);
-                            tm_st16(tO + c * 32 + 16 * h, u);
-                        }
-                    }
-                }
-                const float ref = m == -INFINITY ? 0.f : m;
-                const uint64_t ref2 = pack2f(-ref, -ref);
-                const float4* v4 = reinterpret_cast<const float4*>(vs + vr.slot * kTK);
-                uint64_t sum = 0;
-#pragma unroll
-                for (int c = 0; c < kTK / 32; ++c) {
-                    float f[32];
-                    tm_ld32(tS + c * 32, f);
-                    uint32_t w[16];
-                    const uint32_t see = masked ? (uint32_t)((c < 2 ? see0 : see1) >> (c & 1) * 32) : ~0u;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        uint64_t k2[2] = {scale2, scale2};
-                        if constexpr (kFp8) {
-                            const float4 k = k4[c * 8 + u];
-                            k2[0] = pack2f(k.x, k.y), k2[1] = pack2f(k.z, k.w);
-                            mul2(k2[0], scale2);
-                            mul2(k2[1], scale2);
-                        }
-                        uint64_t e2[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint64_t a = ref2;
-                            fma2(a, pack2f(f[4 * u + 2 * h], f[4 * u + 2 * h + 1]), k2[h]);
-                            float e0, e1;
-                            unpack2f(a, e0, e1);
-                            e0 = ex2(e0), e1 = ex2(e1);
-                            if (masked) {
-                                e0 = see >> (4 * u + 2 * h) & 1 ? e0 : 0.f;
-                                e1 = see >> (4 * u + 2 * h + 1) & 1 ? e1 : 0.f;
-                            }
-                            e2[h] = pack2f(e0, e1);
-                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(e2[h]));
-                        }
-                        if constexpr (kFp8) {
-                            const float4 v = v4[c * 8 + u];
-                            mul2(e2[0], pack2f(v.x, v.y));
-                            mul2(e2[1], pack2f(v.z, v.w));
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float e0, e1;
-                            unpack2f(e2[h], e0, e1);
-                            w[2 * u + h] = Mma<TM>::pack(e0, e1);
-                        }
-                    }
-                    tm_st16(tS + c * 16, w);
-                }
-                float s0, s1;
-                unpack2f(sum, s0, s1);
-                l += s0 + s1;
-                tm_wait_st();
+                softmax_tile<TM, D, kFp8>(tS, tO, k4, v4, vref, scale, masked, see0, see1, i == 0, st);
             }
             tc_before();
             __syncwarp();
             if (lane == 0) arrive(bars + 8 * (kPFull + s));
+            if (issues) {
+                products.pv(i);
+                if (i + 1 < count) products.qk(i + 1);
+            }
+            __syncwarp();
             // ring places of the stream's next tile
             vr.next();
             if (!pl.two) vr.next();
@@ -684,12 +733,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             if (kslot >= (pl.two ? 3 : 4)) kslot -= pl.two ? 3 : 4;
         }
         if (count > 0) wait(bars + 8 * (kOFull + s), 0, &ctrl->dead);
+        if (ctrl->dead) {   // what was issued has to be complete before TMEM is freed
+            const uint64_t t0 = global_ns();
+            while (count > 0 && !try_wait(bars + 8 * (kOFull + s), 0) && global_ns() - t0 < kGiveUpNs) {
+            }
+        }
         tc_after();
     }
     __syncthreads();
 
     // ---- the end: rows of one stream, or of both merged through shared memory
-    float* st = reinterpret_cast<float*>(smem);   // [D][128] of stream 1, then m, l, vref
+    float* other = reinterpret_cast<float*>(smem);   // [D][128] of stream 1, then m, l, vref
     const uint32_t tO = tmem + lanes + 2 * kTK + s * D;
     if (!pl.two && warp >= 4 && warp < 8 && pl.count(1) > 0) {
 #pragma unroll 1
@@ -697,11 +751,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             float f[32];
             tm_ld32(tO + c * 32, f);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) st[(c * 32 + u) * 128 + (tid & 127)] = f[u];
+            for (int u = 0; u < 32; ++u) other[(c * 32 + u) * 128 + (tid & 127)] = f[u];
         }
-        st[D * 128 + (tid & 127)] = m;
-        st[(D + 1) * 128 + (tid & 127)] = l;
-        st[(D + 2) * 128 + (tid & 127)] = vref;
+        other[D * 128 + (tid & 127)] = st.m;
+        other[(D + 1) * 128 + (tid & 127)] = st.l;
+        other[(D + 2) * 128 + (tid & 127)] = st.vref;
     }
     __syncthreads();
     const bool dead = ctrl->dead != 0;
@@ -709,17 +763,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         // with one row tile, stream 1 has the second one's rows here: all dead
         const int row = row0 + 128 * s + (tid & 127);
         const bool join = !pl.two && s == 0 && pl.count(1) > 0;
-        float a0 = 1.f, a1 = 0.f, M = m, den = l;
+        float a0 = 1.f, a1 = 0.f, M = st.m, den = st.l;
         if (join) {
-            const float m1 = st[D * 128 + tid], l1 = st[(D + 1) * 128 + tid];
-            M = fmaxf(m, m1);
+            const float m1 = other[D * 128 + tid], l1 = other[(D + 1) * 128 + tid];
+            M = fmaxf(st.m, m1);
             const float ref = M == -INFINITY ? 0.f : M;
-            a0 = m == -INFINITY ? 1.f : ex2(m - ref);   // (a stream that saw no key has sums 0, or NaN)
+            a0 = st.m == -INFINITY ? 1.f : ex2(st.m - ref);   // (a stream that saw no key has sums 0, or NaN)
             a1 = m1 == -INFINITY ? 1.f : ex2(m1 - ref);
-            den = a0 * l + a1 * l1;
-            if (kFp8) a1 *= st[(D + 2) * 128 + tid];
+            den = a0 * st.l + a1 * l1;
+            if (kFp8) a1 *= other[(D + 2) * 128 + tid];
         }
-        if (kFp8) a0 *= vref;
+        if (kFp8) a0 *= st.vref;
         if (pl.n == 0) den = 0.f;
         bool any = den != 0.f;   // NaN where a score was
         if (row >= last_row) any = false;
@@ -756,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             for (int u = 0; u < 32; ++u) f[u] *= a0;
             if (join) {
 #pragma unroll
-                for (int u = 0; u < 32; ++u) f[u] = fmaf(a1, st[(c * 32 + u) * 128 + tid], f[u]);
+                for (int u = 0; u < 32; ++u) f[u] = fmaf(a1, other[(c * 32 + u) * 128 + tid], f[u]);
             }
             if (bad) {
                 const char* v = p.vd + x.b * p.vd_b + x.hk * p.vd_h;
@@ -794,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 12)
+    if (warp == 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
