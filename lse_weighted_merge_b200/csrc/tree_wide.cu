@@ -9,7 +9,7 @@
 //   * up to 128 rows: both streams have the same rows, stream s the key tiles
 //     s, s + 2, ...; their states are merged at the end, in shared memory.
 // Warps 0-3 and 4-7 are the softmax of stream 0 and 1 (thread = query row = TMEM
-// lane; one thread of each also issues the stream's products), warps 8-11 bring
+// lane; one thread of each also issues the stream's products), warps 8-15 bring
 // the tiles:
 //   S = Q K^T   128 x 128, Q and K in shared memory (K-major, 128-byte swizzle)
 //   O += P V    128 x D, P in TMEM over S (16 bits, half its columns), V in shared
@@ -47,9 +47,14 @@ namespace lsem {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 12 * 32;
+constexpr int kLoadWarps = 8;
+constexpr int kThreads = (8 + kLoadWarps) * 32;
+// Registers per thread of the softmax and of the loading warps: together what the
+// block is launched with, 65536.
+constexpr int kSoftRegs = 184, kLoadRegs = 72;
+static_assert(256 * kSoftRegs + kLoadWarps * 32 * kLoadRegs <= 65536 && kThreads * 128 == 65536, "registers");
 constexpr int kTK = 128;                    // keys per tile
-constexpr uint64_t kGiveUpNs = 2000000000;  // longest wait for another warp
+constexpr int64_t kGiveUpClocks = 4000000000;  // longest wait for another warp, about 2 s
 
 // CTAs of which a wait ran out (their rows are NaN).
 __device__ unsigned g_gave_up;
@@ -68,14 +73,17 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Wait for phase `parity`; once a wait has run out, none waits any more.
+// Barrier of the softmax warps.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Wait for phase `parity`; once a wait has run out, none waits any more.  (By the
+// SM's clock: a read of the global timer takes about as long as a tile's softmax.)
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* dead) {
     if (try_wait(bar, parity)) return;
-    const uint64_t t0 = global_ns();
+    const int64_t t0 = clock64();
     while (*dead == 0) {
         for (int i = 0; i < 16; ++i)
             if (try_wait(bar, parity)) return;
-        if (global_ns() - t0 > kGiveUpNs) *dead = 1;
+        if (clock64() - t0 > kGiveUpClocks) *dead = 1;
     }
 }
 
@@ -127,6 +135,12 @@ __device__ __forceinline__ void tm_put32(uint32_t at, const float (&f)[32]) {
         LSEM_OP32("f", f)
         : "memory");
 }
+// One thread of the (converged) warp, in a form that lets the branch be uniform.
+__device__ __forceinline__ bool elect() {
+    uint32_t yes;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {   // results below 2^-126 are 0
     float y;
@@ -165,15 +179,18 @@ struct Lay {
 };
 
 // Barriers, 8 bytes each, at the control block.
-enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 15, kOFull = 17, kBars = 19 };
+enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 15, kOFull = 17, kStart = 19, kBars = 20 };
 
 struct Ctrl {
     uint64_t bar[kBars];
     uint32_t tmem;
     int dead;
     int bad;            // a value of the drafts is no number
-    float vref[2];      // of the weights, by value slot
-    float top[2][4];
+    // e4m3, known with a tile's keys: the power of two that these were scaled by
+    // (0: their scores still need the scales), the reference of the values' scales,
+    // and whether the tile's values are relative to it already
+    float kref[3], vref[3];
+    int vplain[3];
 };
 static_assert(sizeof(Ctrl) <= 256, "control block");
 
@@ -220,25 +237,50 @@ __device__ __forceinline__ Keys keys_of(const TreeParams& p, const Shard& x, con
     return t;
 }
 
-// Item i of the loaders' order K0, K1, V0, K2, V1, ..., V(n-1): tile and kind.
-__device__ __forceinline__ void item_of(int i, int n, int& j, bool& value) {
-    if (i == 0) {
-        j = 0, value = false;
-    } else if (i == 2 * n - 1) {
-        j = n - 1, value = true;
-    } else {
-        j = (i + 1) >> 1, value = !(i & 1);
-        if (value) j -= 1;
+// Brings the keys and values of tiles still to come into L2, kTilesAhead before
+// they are fetched: one thread per row, threads 0-127 keys, 128-255 values.
+constexpr int kTilesAhead = 4;
+struct Prefetch {
+    const char *at, *scale;
+    int64_t step, scale_step;
+    int key, hi;
+    __device__ __forceinline__ Prefetch(const TreeParams& p, const Shard& x, int tid, bool fp8) {
+        const bool value = tid >= kTK;
+        key = x.lo + (tid & (kTK - 1));
+        hi = x.hi;
+        at = (value ? x.vb : x.kb) + key * (value ? p.v_l : p.k_l);
+        step = kTK * (value ? p.v_l : p.k_l);
+        scale = nullptr;
+        scale_step = 0;
+        if (fp8) {
+            scale = reinterpret_cast<const char*>(value ? p.vs + x.b * p.vs_b + x.hk * p.vs_h + key * p.vs_l
+                                                        : p.ks + x.b * p.ks_b + x.hk * p.ks_h + key * p.ks_l);
+            scale_step = 4 * kTK * (value ? p.vs_l : p.ks_l);
+        }
     }
-}
+    template <int kRowBytes, bool kScale>
+    __device__ __forceinline__ void next() {
+        if (key < hi) {
+#pragma unroll
+            for (int b = 0; b < kRowBytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+            if (kScale) asm volatile("prefetch.global.L2 [%0];" ::"l"(scale));
+        }
+        at += step;
+        if (kScale) scale += scale_step;
+        key += kTK;
+    }
+};
 
+// The loaders bring K0, V0, K1, V1, ...
 template <typename T, int D>
 __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, const WidePlan& pl, unsigned char* smem,
                                        uint32_t smem_u, Ctrl* ctrl, uint32_t bars, int tid) {
     using L = Lay<D>;
-    constexpr int CPR = D / 8, kRows = 128 / CPR, kPending = 3;
+    constexpr int CPR = D / 8, kRows = kLoadWarps * 32 / CPR, kPending = 3;
     const int ch = tid % CPR, row0 = tid / CPR, items = 2 * pl.n;
     Ring kr{pl.two ? 2 : 3, 0, 1}, vr{3, 0, 1};
+    Prefetch pf(p, x, tid, false);
+    for (int i = 0; i < kTilesAhead; ++i) pf.next<2 * D, false>();
     uint32_t pend[kPending];   // full barriers of the items in flight, oldest first
     int np = 0;
 #pragma unroll
@@ -256,9 +298,9 @@ __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, cons
         np = keep;
     };
     for (int i = 0; i < items; ++i) {
-        int j;
-        bool value;
-        item_of(i, pl.n, j, value);
+        const int j = i >> 1;
+        const bool value = i & 1;
+        if (!value) pf.next<2 * D, false>();
         Ring& r = value ? vr : kr;
         const uint32_t empty = bars + 8 * ((value ? kVEmpty : kKEmpty) + r.slot);
         if (!__all_sync(kFull, try_wait(empty, r.phase))) {
@@ -283,10 +325,12 @@ __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, cons
             }
             if (bad) ctrl->bad = 1;
         } else {
-#pragma unroll 4
+            const char* at = src + (t.key0 + row0) * stride;
+#pragma unroll
             for (int row = row0; row < kTK; row += kRows) {
                 const bool ok = row < t.count;
-                cp_async16(dst + L::at(row, ch), src + (t.key0 + (ok ? row : 0)) * stride, ok ? 16 : 0);
+                cp_async16(dst + L::at(row, ch), ok ? at : src, ok ? 16 : 0);
+                at += kRows * stride;
             }
         }
         cp_commit();
@@ -305,92 +349,140 @@ template <int D>
 __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const WidePlan& pl, unsigned char* smem,
                                       uint32_t smem_u, Ctrl* ctrl, uint32_t bars, float* ks, float* vs, int tid) {
     using L = Lay<D>;
-    constexpr int CPR = D / 16, N = kTK * CPR / 128, kRows = 128 / CPR;
-    const int ch = tid % CPR, row0 = tid / CPR, items = 2 * pl.n, raws = pl.two ? 2 : 3, nks = pl.two ? 3 : 4;
-    const int lane = tid & 31, warp = tid >> 5;
-    Ring kr{2, 0, 1}, vr{2, 0, 1};
-    float run = 1.17549435e-38f;   // the reference of the values' scales
-    // raw slots 0 and 1 behind the tiles, 2 where the second tile of queries would be
-    auto raw = [&](int i) -> uint32_t { return (uint32_t)(i < 2 ? 6 * L::kTile + i * L::kRaw : L::kTile) + tid * 16; };
-    auto fetch = [&](int i, int slot) {
-        if (i < items) {
-            int j;
-            bool value;
-            item_of(i, pl.n, j, value);
-            const Keys t = keys_of(p, x, pl, j);
-            const char* src = (value ? t.v : t.k) + ch * 16;
-            const int64_t stride = value ? t.vl : t.kl;
-            const uint32_t dst = smem_u + raw(slot);
+    constexpr int kWarpRows = 512 / D;                  // a warp's 32 chunks of 16 codes
+    constexpr int kStep = kLoadWarps * kWarpRows, N = kTK / kStep;
+    const int lane = tid & 31, warp = tid >> 5, ahead = pl.two ? 1 : 2;
+    const int row0 = warp * kWarpRows + lane * 16 / D, col = lane * 16 % D;
+    // Codes come as they are into 2 or 4 raw tiles: two behind the tiles, two where
+    // the second tile of queries would be.  A warp converts what it fetched.
+    auto raw = [&](int value, int j) -> uint32_t {
+        return (uint32_t)(((j & (ahead - 1)) ? L::kTile : 6 * L::kTile) + value * L::kRaw + warp * 512);
+    };
+    struct Source {
+        const char *base, *at;
+        int64_t step;
+        int key;
+    };
+    auto fetch = [&](Source& f, uint32_t dst) {
 #pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const int row = row0 + u * kRows;
-                const bool ok = row < t.count;
-                cp_async16(dst + u * 2048, src + (t.key0 + (ok ? row : 0)) * stride, ok ? 16 : 0);
-            }
+        for (int u = 0; u < N; ++u) {
+            const bool ok = f.key < x.hi;
+            cp_async16(smem_u + dst + u * kLoadWarps * 512 + lane * 16, ok ? f.at : f.base, ok ? 16 : 0);
+            f.at += f.step;
+            f.key += kStep;
         }
         cp_commit();
     };
-    const float* ksrc = p.ks + x.b * p.ks_b + x.hk * p.ks_h;
-    const float* vsrc = p.vs + x.b * p.vs_b + x.hk * p.vs_h;
-    auto scale_at = [&](const float* src, int64_t stride, int j) -> float {   // of key tid of tile j
-        const int key = x.lo + j * kTK + tid;
-        return j < pl.n && key < x.hi ? src[key * stride] : 0.f;
-    };
-    int rs = 0, item = 0;
-    // the next item's codes -> f16 in place `r` of its ring
-    auto convert = [&](bool value, Ring& r) {
-        unsigned char* tile = smem + (value ? 4 + r.slot : 2 + r.slot) * L::kTile;
-        const unsigned char* src = smem + raw(rs);
+    // A tile's scales, lane l keys l, l + 32, l + 64, l + 96 (0: no key), brought a
+    // tile ahead by every warp for itself.
+    struct Scales {
+        const float* src;
+        int64_t stride;
+        int key;
+        float v[4];
+        __device__ __forceinline__ void next(int hi) {
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const uint4 c = *reinterpret_cast<const uint4*>(src + u * 2048);
-            const uint4 lo = make_uint4(e4m3x2_f16x2(c.x), e4m3x2_f16x2_hi(c.x), e4m3x2_f16x2(c.y), e4m3x2_f16x2_hi(c.y));
-            const uint4 hi = make_uint4(e4m3x2_f16x2(c.z), e4m3x2_f16x2_hi(c.z), e4m3x2_f16x2(c.w), e4m3x2_f16x2_hi(c.w));
-            const int row = row0 + u * kRows;
-            // lanes of the upper half of a row store their two chunks the other
-            // way round: 8 neighbours then hit 8 different groups of banks
-            const int odd = ch >> 2 & 1;
-            *reinterpret_cast<uint4*>(tile + L::at(row, 2 * ch + odd)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(tile + L::at(row, 2 * ch + 1 - odd)) = odd ? lo : hi;
+            for (int e = 0; e < 4; ++e) v[e] = key + 32 * e < hi ? src[(key + 32 * e) * stride] : 0.f;
+            key += kTK;
+        }
+        // The largest and smallest, and whether all are powers of two.
+        __device__ __forceinline__ bool survey(float& big, float& small) const {
+            uint32_t hi = 0, lo = ~0u, frac = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = __float_as_uint(v[e]);
+                hi = max(hi, b);
+                lo = min(lo, b - 1);   // 0 becomes the largest
+                frac |= b;
+            }
+            big = __uint_as_float(__reduce_max_sync(kFull, hi));
+            small = __uint_as_float(__reduce_min_sync(kFull, lo) + 1);
+            return (__reduce_or_sync(kFull, frac) & 0x807fffffu) == 0;
+        }
+    };
+    // mul: the rows are multiplied by their scales times inv
+    auto convert = [&](unsigned char* tile, uint32_t from, bool mul, const Scales& sc, float inv) {
+        const unsigned char* src = smem + from + lane * 8;
+        uint2 c[2 * N];
+#pragma unroll
+        for (int u = 0; u < 2 * N; ++u)
+            c[u] = *reinterpret_cast<const uint2*>(src + (u >> 1) * kLoadWarps * 512 + (u & 1) * 256);
+#pragma unroll
+        for (int u = 0; u < 2 * N; ++u) {
+            const int within = warp * kWarpRows + (u & 1) * (256 / D) + lane * 8 / D;   // below kStep
+            uint32_t h[4] = {e4m3x2_f16x2(c[u].x), e4m3x2_f16x2_hi(c[u].x), e4m3x2_f16x2(c[u].y), e4m3x2_f16x2_hi(c[u].y)};
+            if (mul) {
+                const float mine = D == 128 ? sc.v[u >> 1] : warp & 4 ? sc.v[(u & 2) + 1] : sc.v[u & 2];
+                const float f = __shfl_sync(kFull, mine, within & 31) * inv;
+                const uint32_t f2 = Mma<__half>::pack(f, f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f2));
+            }
+            *reinterpret_cast<uint4*>(tile + L::at((u >> 1) * kStep + within, lane & (D / 8 - 1))) =
+                make_uint4(h[0], h[1], h[2], h[3]);
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) arrive(bars + 8 * ((value ? kVFull : kKFull) + r.slot));
-        r.next();
-        fetch(item + raws, rs);
-        ++item;
-        if (++rs == raws) rs = 0;
     };
-    auto landed = [&]() {
+    auto landed = [&]() {   // the oldest tile's codes, for the whole warp
         if (pl.two)
             cp_wait<1>();
         else
-            cp_wait<2>();
+            cp_wait<3>();
+        __syncwarp();
     };
-    for (int i = 0; i < raws; ++i) fetch(i, i);
-    // the scales come a whole tile ahead
-    float ksc = scale_at(ksrc, p.ks_l, 0), vsc = scale_at(vsrc, p.vs_l, 0);
-    for (int j = -1; j < pl.n; ++j) {
-        if (j + 1 < pl.n) {
-            landed();
-            wait(bars + 8 * (kKEmpty + kr.slot), kr.phase, &ctrl->dead);
-            ks[(j + 1) % nks * kTK + tid] = ksc;
-            ksc = scale_at(ksrc, p.ks_l, j + 2);
-            convert(false, kr);
-        }
-        if (j >= 0) {
-            landed();
-            wait(bars + 8 * (kVEmpty + vr.slot), vr.phase, &ctrl->dead);
-            const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(vsc));
-            if (lane == 0) ctrl->top[j & 1][warp] = __uint_as_float(top);
-            asm volatile("bar.sync 2, 128;" ::: "memory");
-            const float* tp = ctrl->top[j & 1];
-            run = fmaxf(run, pow2_below(fmaxf(fmaxf(tp[0], tp[1]), fmaxf(tp[2], tp[3]))));
-            vs[vr.slot * kTK + tid] = vsc * pow2_inverse(run);
-            if (tid == 0) ctrl->vref[vr.slot] = run;
-            vsc = scale_at(vsrc, p.vs_l, j + 1);
-            convert(true, vr);
-        }
+    Source k{x.kb + col, x.kb + (x.lo + row0) * p.k_l + col, kStep * p.k_l, x.lo + row0};
+    Source v{x.vb + col, x.vb + (x.lo + row0) * p.v_l + col, kStep * p.v_l, x.lo + row0};
+    Prefetch pf(p, x, tid, true);
+    for (int i = 0; i < kTilesAhead; ++i) pf.next<D, true>();
+    for (int j = 0; j < ahead; ++j) {
+        fetch(k, raw(0, j));
+        fetch(v, raw(1, j));
+    }
+    Ring kr{2, 0, 1}, vr{2, 0, 1};
+    float run = 1.17549435e-38f;   // the reference of the values' scales
+    Scales sk{p.ks + x.b * p.ks_b + x.hk * p.ks_h, p.ks_l, x.lo + lane, {}};
+    Scales sv{p.vs + x.b * p.vs_b + x.hk * p.vs_h, p.vs_l, x.lo + lane, {}};
+    sk.next(x.hi);
+    sv.next(x.hi);
+    int kslot = 0;
+    // the first warp keeps the scales that are not in the tile
+    auto keep = [&](float* at, const Scales& sc) {
+        if (warp != 0) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[lane + 32 * e] = sc.v[e];
+    };
+    for (int j = 0; j < pl.n; ++j) {
+        pf.next<D, true>();
+        // f16 has codes * 2^-15 .. 1 exactly: scales that are powers of two go into the tile
+        float kbig, vbig, small;
+        bool kplain = sk.survey(kbig, small);
+        kplain = kplain && small >= kbig * 3.0517578e-05f && kbig >= 1.17549435e-38f && kbig <= 8.507059e37f;
+        bool vplain = sv.survey(vbig, small);
+        run = fmaxf(run, pow2_below(vbig));
+        vplain = vplain && small >= run * 3.0517578e-05f && small >= 1.17549435e-38f && vbig <= run;
+        landed();
+        wait(bars + 8 * (kKEmpty + kr.slot), kr.phase, &ctrl->dead);
+        convert(smem + (2 + kr.slot) * L::kTile, raw(0, j), kplain, sk, pow2_inverse(pow2_below(kbig)));
+        // (the place of three tiles ago: the values of two tiles ago would not be
+        // in if that tile's softmax were not over)
+        if (!kplain) keep(ks + kslot * kTK, sk);
+        if (tid == 0) ctrl->kref[kslot] = kplain ? kbig : 0.f, ctrl->vref[kslot] = run, ctrl->vplain[kslot] = vplain;
+        __syncwarp();
+        if (lane == 0) arrive(bars + 8 * (kKFull + kr.slot));
+        kr.next();
+        if (++kslot == 3) kslot = 0;
+        sk.next(x.hi);
+        fetch(k, raw(0, j));
+        landed();
+        wait(bars + 8 * (kVEmpty + vr.slot), vr.phase, &ctrl->dead);
+        convert(smem + (4 + vr.slot) * L::kTile, raw(1, j), vplain, sv, pow2_inverse(run));
+        if (!vplain) keep(vs + vr.slot * kTK, sv);
+        __syncwarp();
+        if (lane == 0) arrive(bars + 8 * (kVFull + vr.slot));
+        vr.next();
+        sv.next(x.hi);
+        fetch(v, raw(1, j));
     }
     cp_wait<0>();
 }
@@ -409,28 +501,27 @@ struct Products {
 
     __device__ __forceinline__ void qk(int i) const {
         const int j = pl.tile(s, i), nk = kFp8 || pl.two ? 2 : 3, slot = j % nk;
+        const uint64_t q = smem_desc(smem_u + (pl.two ? s : 0) * L::kTile, 16);
+        const uint64_t k = smem_desc(smem_u + (slot < 2 ? 2 + slot : 1) * L::kTile, 16);
         wait(bars + 8 * (kKFull + slot), (uint32_t)(j / nk) & 1u, &ctrl->dead);
         tc_after();
-        const uint32_t q = smem_u + (pl.two ? s : 0) * L::kTile;
-        const uint32_t k = smem_u + (slot < 2 ? 2 + slot : 1) * L::kTile;
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            const uint32_t off = (u >> 2) * L::kBlock + (u & 3) * 32;
-            mma_ss(tmem + s * kTK, smem_desc(q + off, 16), smem_desc(k + off, 16), kIdQK, u > 0);
+        for (int u = 0; u < D / 16; ++u) {   // (descriptors count in 16 bytes)
+            const uint32_t off = ((u >> 2) * L::kBlock + (u & 3) * 32) >> 4;
+            mma_ss(tmem + s * kTK, q + off, k + off, kIdQK, u > 0);
         }
-        tc_commit(bars + 8 * (kKEmpty + slot));
         tc_commit(bars + 8 * (kSFull + s));
+        tc_commit(bars + 8 * (kKEmpty + slot));
     }
     __device__ __forceinline__ void pv(int i) const {
         const int j = pl.tile(s, i), nv = kFp8 ? 2 : 3, slot = j % nv;
+        const uint64_t v = smem_desc(smem_u + (4 + slot) * L::kTile, L::kBlock);
         wait(bars + 8 * (kVFull + slot), (uint32_t)(j / nv) & 1u, &ctrl->dead);
         wait(bars + 8 * (kPFull + s), (uint32_t)i & 1u, &ctrl->dead);
         tc_after();
-        const uint32_t v = smem_u + (4 + slot) * L::kTile;
 #pragma unroll
         for (int u = 0; u < kTK / 16; ++u)
-            mma_ts(tmem + 2 * kTK + s * D, tmem + s * kTK + u * 8, smem_desc(v + u * 2048, L::kBlock), kIdPV,
-                   i > 0 || u > 0);
+            mma_ts(tmem + 2 * kTK + s * D, tmem + s * kTK + u * 8, v + (u * 2048 >> 4), kIdPV, i > 0 || u > 0);
         tc_commit(bars + 8 * (kVEmpty + slot));
         if (i == pl.count(s) - 1) tc_commit(bars + 8 * (kOFull + s));
     }
@@ -478,116 +569,173 @@ __device__ __forceinline__ void load_query(const char* src, unsigned char* tile,
 
 // ------------------------------------------------------------ softmax
 
-// A row's running state: reference (log2 units, kLow .. kHigh below the maximum),
-// sum of weights, and e4m3: the values' scale that O is relative to.
+// A row's running state: reference (log2 units), sum of weights, by how much the
+// reference is to rise before the next tile, and e4m3: the values' scale that O is
+// relative to.
 struct RowSum {
-    float m, l, vref;
+    float m, l, rise, vref;
 };
+// Weights are watched as the largest sum of 4 of them.  A new reference lies
+// kLow below the maximum.  Past kSoft it rises for the next tile, by a power of
+// two that leaves the sum at 2^kBase to 2^(kBase + 1), the largest weight at a
+// quarter of that or more: f16 weights then stay between 2^7 (which keeps 2^-24 of
+// the largest at f16's 11 bits) and f16's 65504, a value's scale below 2 included.
+// Past kHard the tile's weights are made again.
 template <typename TM>
-constexpr float kLow = std::is_same<TM, __half>::value ? 7.f : 0.f;
-template <typename TM>
-constexpr float kHigh = std::is_same<TM, __half>::value ? 14.f : 8.f;
+struct Bounds {
+    static constexpr bool kHalf = std::is_same<TM, __half>::value;
+    static constexpr float kLow = kHalf ? 7.f : 0.f, kSoft = kHalf ? 2048.f : 1.0995116e12f;
+    static constexpr float kHard = kHalf ? 32000.f : 1e30f;
+    static constexpr int kBase = kHalf ? 9 : 2;
+};
 
-// The weights of 32 scores f, their sum and the largest exponent.  kCareful: a
-// mask, and the scaled score rounded before the reference is subtracted (a fused
-// difference of numbers past 2^22 could lie far from that of the rounded ones,
-// which the reference is made from).
-template <typename TM, bool kFp8, bool kCareful>
-__device__ __forceinline__ void weights32(const float (&f)[32], const float4* k4, const float4* v4, uint64_t scale2,
-                                          uint64_t ref2, uint32_t see, uint64_t& sum, float& top, uint32_t* w) {
+// A tile's scores: where, what multiplies them, which of them the row sees.
+struct Scores {
+    uint32_t at;
+    float scale;             // of the row (and of all keys of the tile)
+    const float4 *k4, *v4;   // e4m3 whose scales are not in the tiles: the keys' (or NULL), the values' (or NULL)
+    float vinv;              // what the values' are multiplied by
+    uint64_t see0, see1;
+};
+
+// Replace the tile's scores by the scaled ones, -inf where not seen: for tiles with
+// a mask or with scales key by key, and where the scores are so large that a fused
+// difference from the reference could lie far from that of the rounded scores.
+template <bool kFp8>
+__device__ __forceinline__ void scale_scores(Scores& x) {
+#pragma unroll 1
+    for (int c = 0; c < kTK; c += 32) {
+        float f[32];
+        tm_ld32(x.at + c, f);
+        const uint32_t see = (uint32_t)((c < 64 ? x.see0 : x.see1) >> (c & 63));
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        uint64_t k2[2] = {scale2, scale2};
-        if constexpr (kFp8) {
-            const float4 k = k4[u];
-            k2[0] = pack2f(k.x, k.y), k2[1] = pack2f(k.z, k.w);
-            mul2(k2[0], scale2);
-            mul2(k2[1], scale2);
-        }
-        uint64_t e2[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint64_t a;
-            float e0, e1;
-            if constexpr (kCareful) {
-                a = pack2f(f[4 * u + 2 * h], f[4 * u + 2 * h + 1]);
-                mul2(a, k2[h]);
-                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(ref2));
-            } else {
-                a = ref2;
-                fma2(a, pack2f(f[4 * u + 2 * h], f[4 * u + 2 * h + 1]), k2[h]);
+        for (int u = 0; u < 32; u += 4) {
+            float k[4] = {x.scale, x.scale, x.scale, x.scale};
+            if (kFp8 && x.k4) {
+                const float4 s = x.k4[(c + u) / 4];
+                k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
             }
-            unpack2f(a, e0, e1);
-            if (kCareful) {
-                e0 = see >> (4 * u + 2 * h) & 1 ? e0 : -INFINITY;
-                e1 = see >> (4 * u + 2 * h + 1) & 1 ? e1 : -INFINITY;
-            }
-            top = fmaxf(top, fmaxf(e0, e1));
-            e2[h] = pack2f(ex2(e0), ex2(e1));
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(e2[h]));
-        }
-        if constexpr (kFp8) {
-            const float4 v = v4[u];
-            mul2(e2[0], pack2f(v.x, v.y));
-            mul2(e2[1], pack2f(v.z, v.w));
-        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float e0, e1;
-            unpack2f(e2[h], e0, e1);
-            w[2 * u + h] = Mma<TM>::pack(e0, e1);
+            for (int e = 0; e < 4; ++e) f[u + e] = see >> (u + e) & 1 ? f[u + e] * k[e] : -INFINITY;
         }
+        tm_put32(x.at + c, f);
     }
+    tm_wait_st();
+    x.scale = 1.f;
 }
 
-// S of one tile (at tS) -> P over it.  The weights are taken relative to the
-// reference that the earlier tiles left, in one pass over S; where the tile's
-// maximum turns out to lie kHigh above it (always in a row's first tile, hardly
-// ever later) the reference moves and the pass is made again.
-template <typename TM, bool kFp8, bool kCareful>
-__device__ __forceinline__ void softmax_pass(uint32_t tS, const float4* k4, const float4* v4, float scale, float ref,
-                                             uint64_t see0, uint64_t see1, float& l, float& top, uint32_t* w) {
-    const uint64_t scale2 = pack2f(scale, scale), ref2 = pack2f(-ref, -ref);
-    uint64_t sum = 0;
+// The largest score, scaled.
+__device__ __forceinline__ float softmax_top(const Scores& x) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kTK; c += 32) {
+        float f[32];
+        tm_ld32(x.at + c, f);
+#pragma unroll
+        for (int u = 0; u < 32; u += 4) top = fmaxf(fmaxf(top, fmaxf(f[u], f[u + 1])), fmaxf(f[u + 2], f[u + 3]));
+    }
+    return top == -INFINITY ? top : top * x.scale;
+}
+
+// Weights relative to ref, as 16-bit pairs, and their sums: `sum` of all, `top` the
+// largest of 4.  kValue: the weights are multiplied by the values' scales.
+template <typename TM, bool kValue>
+__device__ __forceinline__ void weights32(const Scores& x, int c, float (&f)[32], uint64_t scale2, uint64_t ref2,
+                                          uint64_t (&sum)[4], float& top, uint32_t* w) {
+    // in steps over all 32, so that each step's latencies overlap
+    uint64_t a[16], t[4];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        a[u] = ref2;
+        fma2(a[u], pack2f(f[2 * u], f[2 * u + 1]), scale2);
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        float e0, e1;
+        unpack2f(a[u], e0, e1);
+        a[u] = pack2f(ex2(e0), ex2(e1));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        t[u] = a[u];
+#pragma unroll
+        for (int h = 4; h < 16; h += 4) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t[u]) : "l"(a[u + h]));
+        float t0, t1;
+        unpack2f(t[u], t0, t1);
+        top = fmaxf(top, fmaxf(t0, t1));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[u]) : "l"(t[u]));
+    }
+    if (kValue) {
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) {
+            const float4 v = x.v4[c / 4 + u / 2];
+            mul2(a[u], pack2f(v.x * x.vinv, v.y * x.vinv));
+            mul2(a[u + 1], pack2f(v.z * x.vinv, v.w * x.vinv));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        float e0, e1;
+        unpack2f(a[u], e0, e1);
+        w[u] = Mma<TM>::pack(e0, e1);
+    }
+}
+template <typename TM, bool kValue>
+__device__ __forceinline__ float softmax_pass(const Scores& x, float ref, float& top, uint32_t* w) {
+    const uint64_t scale2 = pack2f(x.scale, x.scale), ref2 = pack2f(-ref, -ref);
+    uint64_t sum[4] = {0, 0, 0, 0};
     float fa[32], fb[32];
-    tm_get32(tS, fa);
+    top = 0.f;
+    tm_get32(x.at, fa);
 #pragma unroll
-    for (int c = 0; c < 4; c += 2) {
+    for (int c = 0; c < kTK; c += 64) {
         tm_wait32(fa);
-        tm_get32(tS + 32 * c + 32, fb);
-        weights32<TM, kFp8, kCareful>(fa, k4 + 8 * c, v4 + 8 * c, scale2, ref2, (uint32_t)(c ? see1 : see0), sum, top,
-                                      w + 16 * c);
+        tm_get32(x.at + c + 32, fb);
+        weights32<TM, kValue>(x, c, fa, scale2, ref2, sum, top, w + c / 2);
         tm_wait32(fb);
-        if (c == 0) tm_get32(tS + 64, fa);
-        weights32<TM, kFp8, kCareful>(fb, k4 + 8 * c + 8, v4 + 8 * c + 8, scale2, ref2,
-                                      (uint32_t)((c ? see1 : see0) >> 32), sum, top, w + 16 * c + 16);
+        if (c == 0) tm_get32(x.at + 64, fa);
+        weights32<TM, kValue>(x, c + 32, fb, scale2, ref2, sum, top, w + c / 2 + 16);
     }
-    float s0, s1;
-    unpack2f(sum, s0, s1);
-    l = s0 + s1;
+    float s[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) unpack2f(sum[u], s[2 * u], s[2 * u + 1]);
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
+// S of one tile -> P over it.  The weights are taken relative to the reference
+// that the earlier tiles left, in one pass over S; where they turn out too large
+// (hardly ever) or the row has no reference yet, the maximum is looked up, the
+// reference moves and the pass is made again.
 template <typename TM, int D, bool kFp8>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, const float4* k4, const float4* v4, float vref,
-                                             float scale, bool masked, uint64_t see0, uint64_t see1, bool first,
-                                             RowSum& st) {
+__device__ __forceinline__ void softmax_tile(Scores x, uint32_t tO, float vref, bool scaled, bool first, RowSum& st) {
+    using Bd = Bounds<TM>;
     uint32_t w[kTK / 2];
-    float down = 1.f, l;
+    float l, top, down = 1.f;
+    if (st.rise > 0.f) st.m += st.rise, down = ex2(-st.rise);
+    if (scaled) scale_scores<kFp8>(x);
+    bool move = st.m == -INFINITY, moved = false;
     for (;;) {
-        const float ref = st.m == -INFINITY ? 0.f : st.m;
-        float top = -INFINITY;
-        if (masked || __any_sync(kFull, fabsf(ref) > 4194304.f))
-            softmax_pass<TM, kFp8, true>(tS, k4, v4, scale, ref, see0, see1, l, top, w);
-        else
-            softmax_pass<TM, kFp8, false>(tS, k4, v4, scale, ref, see0, see1, l, top, w);
-        const float next = top + ref - kLow<TM>;
-        const bool move = st.m == -INFINITY ? top != -INFINITY : top > kHigh<TM> && next != st.m;
-        if (!__any_sync(kFull, move)) break;
-        if (move) {
-            down *= ex2(st.m - next);   // 0 at first
-            st.m = next;
+        if (__any_sync(kFull, move)) {
+            const float next = softmax_top(x) - Bd::kLow;
+            if (move && next != -INFINITY) {
+                down *= ex2(st.m - next);   // 0 at first
+                st.m = next;
+            }
+            moved = moved || move;   // once: past 2^26 the reference has no finer steps
         }
+        const float ref = st.m == -INFINITY ? 0.f : st.m;
+        if (!scaled && __any_sync(kFull, fabsf(ref) > 4194304.f)) {
+            scale_scores<kFp8>(x);
+            scaled = true;
+        }
+        if (kFp8 && x.v4)
+            l = softmax_pass<TM, true>(x, ref, top, w);
+        else
+            l = softmax_pass<TM, false>(x, ref, top, w);
+        move = top > Bd::kHard && !moved;
+        if (!__any_sync(kFull, move)) break;
     }
+    st.rise = top > Bd::kSoft ? (float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase) : 0.f;
     st.l = st.l * down + l;
     if constexpr (kFp8) {
         down *= st.vref * pow2_inverse(vref);
@@ -608,7 +756,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, const flo
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(w[32 * c + e]);
-        tm_put32(tS + 32 * c, f);
+        tm_put32(x.at + 32 * c, f);
     }
     tm_wait_st();
 }
@@ -623,9 +771,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     const uint32_t smem_u = smem_u32(smem);
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + L::kCtrl);
     const uint32_t bars = smem_u + L::kCtrl;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
 
-    if (warp == 8) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctrl->tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -641,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     pl.cached = last_row > row0 ? (x.hi - x.lo + kTK - 1) / kTK : 0;
     pl.n = pl.cached + (p.fold && r == p.R - 1 && last_row > row0 ? 1 : 0);
     // the scales' rings: keys' by tile, values' by slot
-    float* ks = reinterpret_cast<float*>(pl.two ? smem + L::kCtrl + 256 : smem + L::kTile + L::kRaw);
-    float* vs = ks + (pl.two ? 3 : 4) * kTK;
+    float* ks = reinterpret_cast<float*>(smem + L::kCtrl + 256);
+    float* vs = ks + 3 * kTK;
     if (tid == 0) {
         auto init = [&](int b, int n) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * b), "r"(n) : "memory");
@@ -650,10 +798,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         const int users = pl.two ? 2 : 1;   // streams that read a tile
         init(kQFull, 8);
         for (int i = 0; i < 3; ++i) {
-            init(kKFull + i, 4), init(kKEmpty + i, users);
-            init(kVFull + i, 4), init(kVEmpty + i, users);
+            init(kKFull + i, kLoadWarps), init(kKEmpty + i, users);
+            init(kVFull + i, kLoadWarps), init(kVEmpty + i, users);
         }
         for (int s = 0; s < 2; ++s) init(kSFull + s, 1), init(kPFull + s, 4), init(kOFull + s, 1);
+        init(kStart, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ctrl->dead = (smem_u & 1023u) != 0;   // the swizzle's atoms are 1024 bytes
         ctrl->bad = 0;
@@ -666,15 +815,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     const int s = warp >> 2 & 1;                        // softmax warps: the stream
     const int row = row0 + (pl.two ? 128 * s : 0) + (tid & 127);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's lanes of TMEM
-    RowSum st{-INFINITY, 0.f, 1.17549435e-38f};
+    RowSum st{-INFINITY, 0.f, 0.f, 1.17549435e-38f};
     uint64_t word = 0;
 
     if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         if constexpr (kFp8)
             load8<D>(p, x, pl, smem, smem_u, ctrl, bars, ks, vs, tid - 256);
         else
             load16<T, D>(p, x, pl, smem, smem_u, ctrl, bars, tid - 256);
-    } else {
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    {
         float scale = fabsf(p.scale_log2);
         if (pl.n > 0) {
             const char* src = row < last_row ? q_row(p, x.b, x.hk, row) : nullptr;
@@ -688,12 +841,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         const bool idle = row - lane >= last_row;   // no live row in the warp
         const uint32_t tS = tmem + lanes + s * kTK, tO = tmem + lanes + 2 * kTK + s * D;
         const Products<TM, D, kFp8> products{pl, smem_u, tmem, bars, ctrl, s};
-        const bool issues = (warp & 3) == 0 && lane == 0;
+        const bool issues = (warp & 3) == 0;
         const int count = pl.count(s);
         Ring vr{2, pl.two ? 0 : s, 0};
         int kslot = pl.two ? 0 : s;
-        if (issues && count > 0) {
+        if (issues && count > 0 && elect()) {
             wait(bars + 8 * kQFull, 0, &ctrl->dead);
+            if (s == 1) wait(bars + 8 * kStart, 0, &ctrl->dead);
             products.qk(0);
         }
         __syncwarp();
@@ -708,20 +862,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             wait(bars + 8 * (kSFull + s), (uint32_t)i & 1u, &ctrl->dead);
             tc_after();
             if (!idle) {
-                const float4* k4 = reinterpret_cast<const float4*>(ks + kslot * kTK);
-                const float4* v4 = reinterpret_cast<const float4*>(vs + vr.slot * kTK);
+                Scores sc{tS, scale, nullptr, nullptr, 0.f, see0, see1};
                 float vref = 1.f;
+                bool scaled = masked;
                 if constexpr (kFp8) {
-                    wait(bars + 8 * (kVFull + vr.slot), vr.phase, &ctrl->dead);   // the values' scales
-                    vref = ctrl->vref[vr.slot];
+                    const float kref = ctrl->kref[kslot];
+                    vref = ctrl->vref[kslot];
+                    if (kref != 0.f)
+                        sc.scale *= kref;
+                    else
+                        sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK);
+                    if (!ctrl->vplain[kslot]) {
+                        wait(bars + 8 * (kVFull + vr.slot), vr.phase, &ctrl->dead);   // the values' scales
+                        sc.v4 = reinterpret_cast<const float4*>(vs + vr.slot * kTK);
+                        sc.vinv = pow2_inverse(vref);
+                    }
+                    scaled = scaled || sc.k4;
                     __syncwarp();
                 }
-                softmax_tile<TM, D, kFp8>(tS, tO, k4, v4, vref, scale, masked, see0, see1, i == 0, st);
+                softmax_tile<TM, D, kFp8>(sc, tO, vref, scaled, i == 0, st);
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) arrive(bars + 8 * (kPFull + s));
-            if (issues) {
+            if (lane == 0) {
+                arrive(bars + 8 * (kPFull + s));
+                if (s == 0 && i == 0) arrive(bars + 8 * kStart);
+            }
+            if (issues && elect()) {
                 products.pv(i);
                 if (i + 1 < count) products.qk(i + 1);
             }
@@ -730,22 +897,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             vr.next();
             if (!pl.two) vr.next();
             kslot += pl.two ? 1 : 2;
-            if (kslot >= (pl.two ? 3 : 4)) kslot -= pl.two ? 3 : 4;
+            if (kslot >= 3) kslot -= 3;
         }
         if (count > 0) wait(bars + 8 * (kOFull + s), 0, &ctrl->dead);
         if (ctrl->dead) {   // what was issued has to be complete before TMEM is freed
-            const uint64_t t0 = global_ns();
-            while (count > 0 && !try_wait(bars + 8 * (kOFull + s), 0) && global_ns() - t0 < kGiveUpNs) {
+            const int64_t t0 = clock64();
+            while (count > 0 && !try_wait(bars + 8 * (kOFull + s), 0) && clock64() - t0 < kGiveUpClocks) {
             }
         }
         tc_after();
     }
-    __syncthreads();
+    soft_sync();
 
     // ---- the end: rows of one stream, or of both merged through shared memory
     float* other = reinterpret_cast<float*>(smem);   // [D][128] of stream 1, then m, l, vref
     const uint32_t tO = tmem + lanes + 2 * kTK + s * D;
-    if (!pl.two && warp >= 4 && warp < 8 && pl.count(1) > 0) {
+    if (!pl.two && warp >= 4 && pl.count(1) > 0) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             float f[32];
@@ -757,9 +924,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         other[(D + 1) * 128 + (tid & 127)] = st.l;
         other[(D + 2) * 128 + (tid & 127)] = st.vref;
     }
-    __syncthreads();
+    soft_sync();
     const bool dead = ctrl->dead != 0;
-    if (warp < 8) {
+    {
         // with one row tile, stream 1 has the second one's rows here: all dead
         const int row = row0 + 128 * s + (tid & 127);
         const bool join = !pl.two && s == 0 && pl.count(1) > 0;
@@ -846,9 +1013,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         }
     }
     tc_before();
-    __syncthreads();
+    soft_sync();
     tc_after();
-    if (warp == 8)
+    if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
