@@ -483,11 +483,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) tree_rows16_kernel(const TreeP
     using Draft = Tiles16<T, D>;
     constexpr int kRing = kRowStages * (Cache::kBytes > Draft::kBytes ? Cache::kBytes : Draft::kBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int i = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - i * p.row_tiles) * 16;
+    const int r = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - r * p.row_tiles) * 16;
     const int rows = p.T * p.G;
     pdl_wait();
     pdl_release();
-    Shard x = shard_of(p, p.r0 + i, blockIdx.y, blockIdx.z);
+    Shard x = shard_of(p, r, blockIdx.y, blockIdx.z);
     if (row0 >= x.live * p.G) x.hi = x.lo;   // dead rows only
     RowState<D> w;
     unsigned char* ring = smem + warp * kRing;
@@ -691,16 +691,19 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
     p.T = a.T, p.Hq = a.Hq, p.G = pl.G, p.L = a.L, p.R = a.R;
     // More than 16 rows take the wide kernel.  The drafts of a 16-bit cache are
     // then with its last shard; those of an 8-bit one, whose products are of
-    // another type, stay a shard of the rows16 kernel.
+    // another type, are a shard of an earlier launch, which a lone shard of the
+    // cache merges with itself.
     const bool wide = pl.rows > 16;
     p.fold = wide && !fp8 && drafts;
-    p.shards = p.fold ? a.R : pl.shards;
+    p.join = wide && fp8 && drafts && a.R == 1;
+    p.shards = p.fold ? a.R : p.join ? 1 : pl.shards;
     p.row_tiles = (pl.rows + 15) / 16;
     p.scale_log2 = a.scale * kLog2e;
-    if (p.shards > 1) {
+    if (p.shards > 1 || p.join) {
         p.po = static_cast<float*>(a.workspace);
         p.pl = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + pl.ws_l_off);
-    } else {
+    }
+    if (p.shards == 1) {
         p.out = static_cast<char*>(a.out_o);
         p.out_lse = a.out_lse;
     }
@@ -712,20 +715,26 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = kPdl ? 1 : 0;
     cudaError_t e = cudaSuccess;
-    if (!wide || (fp8 && drafts)) {
-        p.r0 = wide ? a.R : 0;
+    if (wide) {
+        if (fp8 && drafts) {
+            TreeParams d = p;
+            d.r0 = a.R;
+            d.join = 0;
+            e = launch_tree_wide(d, a.dtype, false, 1, a.out_dtype, a.B, a.Hkv, a.D, kPdl != 0, stream);
+        }
+        if (e == cudaSuccess)
+            e = launch_tree_wide(p, a.dtype, fp8, a.R, a.out_dtype, a.B, a.Hkv, a.D, kPdl != 0, stream);
+    } else {
         const TreeKernel k = a.dtype == LSE_MERGE_F16 ? pick_tree<__half>(a.D, fp8, a.out_dtype)
                                                       : pick_tree<__nv_bfloat16>(a.D, fp8, a.out_dtype);
         e = allow_smem((const void*)k.fn, k.smem);
         if (e == cudaSuccess) {
-            cfg.gridDim = dim3((unsigned)(p.row_tiles * (p.shards - p.r0)), (unsigned)a.Hkv, (unsigned)a.B);
+            cfg.gridDim = dim3((unsigned)(p.row_tiles * p.shards), (unsigned)a.Hkv, (unsigned)a.B);
             cfg.blockDim = dim3(kRowWarps * 32);
             cfg.dynamicSmemBytes = (size_t)k.smem;
             e = cudaLaunchKernelEx(&cfg, k.fn, p);
         }
     }
-    if (e == cudaSuccess && wide)
-        e = launch_tree_wide(p, a.dtype, fp8, a.out_dtype, a.B, a.Hkv, a.D, kPdl != 0, stream);
     if (e == cudaSuccess && p.shards > 1) {
         const uint32_t rows = (uint32_t)a.B * a.T * a.Hq, per = 128u / (uint32_t)(a.D / 4);
         cfg.gridDim = dim3((rows + per - 1) / per);

@@ -25,6 +25,7 @@ struct TreeParams {
     int T, Hq, G, L, R, shards, row_tiles;
     int r0;             // shard of the launch's first block
     int fold;           // the last cached shard has the drafts too
+    int join;           // po and pl hold one shard's partials, which the launch merges with its own shard
     int out_dtype;
     float scale_log2;   // scale * log2(e)
     float* po;          // partials [B, T, Hq, shards, D], or NULL:
@@ -34,10 +35,10 @@ struct TreeParams {
 };
 
 // The kernel for more than 16 query rows per (sequence, KV head) (tree_wide.cu):
-// launches the cached shards of p, and of a 16-bit cache the drafts with the
-// last of them.
-cudaError_t launch_tree_wide(const TreeParams& p, int dtype, bool fp8, int out_dtype, int B, int Hkv, int D, bool pdl,
-                             cudaStream_t stream);
+// launches `shards` shards of p from p.r0 on; fp8: the cache is e4m3 (the shard of
+// the drafts, p.R, is 16-bit and of a launch of its own).
+cudaError_t launch_tree_wide(const TreeParams& p, int dtype, bool fp8, int shards, int out_dtype, int B, int Hkv, int D,
+                             bool pdl, cudaStream_t stream);
 
 // cudaFuncSetAttribute(max dynamic shared memory) once per (kernel, device).
 cudaError_t allow_smem(const void* fn, int bytes);

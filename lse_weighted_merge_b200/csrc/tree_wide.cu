@@ -48,12 +48,14 @@ namespace attn {
 namespace {
 
 constexpr int kLoadWarps = 8;
-constexpr int kThreads = (8 + kLoadWarps) * 32;
-// Registers per thread of the softmax and of the loading warps: together what the
-// block is launched with, 65536.
-constexpr int kSoftRegs = 184, kLoadRegs = 72;
-static_assert(256 * kSoftRegs + kLoadWarps * 32 * kLoadRegs <= 65536 && kThreads * 128 == 65536, "registers");
+constexpr int kThreads = (8 + kLoadWarps + 4) * 32;
+// Registers per thread of the softmax, loading and issuing warps: together at most
+// what the block is launched with.
+constexpr int kSoftRegs = 136, kLoadRegs = 80, kIssueRegs = 40, kLaunchRegs = 96;
+static_assert(256 * kSoftRegs + kLoadWarps * 32 * kLoadRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs &&
+              kThreads * kLaunchRegs <= 65536 && kThreads * (kLaunchRegs + 8) > 65536, "registers");
 constexpr int kTK = 128;                    // keys per tile
+constexpr int kHK = 64;                     // keys per step of a stream: half a tile
 constexpr int64_t kGiveUpClocks = 4000000000;  // longest wait for another warp, about 2 s
 
 // CTAs of which a wait ran out (their rows are NaN).
@@ -178,8 +180,8 @@ struct Lay {
     }
 };
 
-// Barriers, 8 bytes each, at the control block.
-enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 15, kOFull = 17, kStart = 19, kBars = 20 };
+// Barriers, 8 bytes each, at the control block: S and P by stream and half.
+enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 17, kODone = 21, kBars = 23 };
 
 struct Ctrl {
     uint64_t bar[kBars];
@@ -188,9 +190,8 @@ struct Ctrl {
     int bad;            // a value of the drafts is no number
     // e4m3, known with a tile's keys: the power of two that these were scaled by
     // (0: their scores still need the scales), the reference of the values' scales,
-    // and whether the tile's values are relative to it already
-    float kref[3], vref[3];
-    int vplain[3];
+    // and whether the tile's values still need theirs
+    float4 tile[3];   // by tile: these three
 };
 static_assert(sizeof(Ctrl) <= 256, "control block");
 
@@ -199,8 +200,27 @@ struct WidePlan {
     bool two;        // two row tiles
     int n;           // key tiles
     int cached;      // of them over the cache; the last may be the drafts
+    int len, live;   // keys of the shard, drafts
     __device__ __forceinline__ int count(int s) const { return two ? n : (n + 1 - s) >> 1; }
     __device__ __forceinline__ int tile(int s, int i) const { return two ? i : 2 * i + s; }
+    __device__ __forceinline__ int keys(int j) const { return j < cached ? min(kTK, len - j * kTK) : live; }
+};
+
+// The halves of a stream's tiles, without those that have no key.
+struct Halves {
+    const WidePlan& pl;
+    int s, i, half, seq;
+    __device__ __forceinline__ Halves(const WidePlan& pl_, int s_) : pl(pl_), s(s_), i(0), half(0), seq(0) {}
+    __device__ __forceinline__ bool more() const { return i < pl.count(s); }
+    __device__ __forceinline__ int tile() const { return pl.tile(s, i); }
+    __device__ __forceinline__ bool ends_tile() const { return half == 1 || pl.keys(tile()) <= kHK; }
+    __device__ __forceinline__ void next() {
+        if (ends_tile())
+            ++i, half = 0;
+        else
+            half = 1;
+        ++seq;
+    }
 };
 
 struct Ring {
@@ -237,40 +257,6 @@ __device__ __forceinline__ Keys keys_of(const TreeParams& p, const Shard& x, con
     return t;
 }
 
-// Brings the keys and values of tiles still to come into L2, kTilesAhead before
-// they are fetched: one thread per row, threads 0-127 keys, 128-255 values.
-constexpr int kTilesAhead = 4;
-struct Prefetch {
-    const char *at, *scale;
-    int64_t step, scale_step;
-    int key, hi;
-    __device__ __forceinline__ Prefetch(const TreeParams& p, const Shard& x, int tid, bool fp8) {
-        const bool value = tid >= kTK;
-        key = x.lo + (tid & (kTK - 1));
-        hi = x.hi;
-        at = (value ? x.vb : x.kb) + key * (value ? p.v_l : p.k_l);
-        step = kTK * (value ? p.v_l : p.k_l);
-        scale = nullptr;
-        scale_step = 0;
-        if (fp8) {
-            scale = reinterpret_cast<const char*>(value ? p.vs + x.b * p.vs_b + x.hk * p.vs_h + key * p.vs_l
-                                                        : p.ks + x.b * p.ks_b + x.hk * p.ks_h + key * p.ks_l);
-            scale_step = 4 * kTK * (value ? p.vs_l : p.ks_l);
-        }
-    }
-    template <int kRowBytes, bool kScale>
-    __device__ __forceinline__ void next() {
-        if (key < hi) {
-#pragma unroll
-            for (int b = 0; b < kRowBytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
-            if (kScale) asm volatile("prefetch.global.L2 [%0];" ::"l"(scale));
-        }
-        at += step;
-        if (kScale) scale += scale_step;
-        key += kTK;
-    }
-};
-
 // The loaders bring K0, V0, K1, V1, ...
 template <typename T, int D>
 __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, const WidePlan& pl, unsigned char* smem,
@@ -279,8 +265,6 @@ __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, cons
     constexpr int CPR = D / 8, kRows = kLoadWarps * 32 / CPR, kPending = 3;
     const int ch = tid % CPR, row0 = tid / CPR, items = 2 * pl.n;
     Ring kr{pl.two ? 2 : 3, 0, 1}, vr{3, 0, 1};
-    Prefetch pf(p, x, tid, false);
-    for (int i = 0; i < kTilesAhead; ++i) pf.next<2 * D, false>();
     uint32_t pend[kPending];   // full barriers of the items in flight, oldest first
     int np = 0;
 #pragma unroll
@@ -300,7 +284,6 @@ __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, cons
     for (int i = 0; i < items; ++i) {
         const int j = i >> 1;
         const bool value = i & 1;
-        if (!value) pf.next<2 * D, false>();
         Ring& r = value ? vr : kr;
         const uint32_t empty = bars + 8 * ((value ? kVEmpty : kKEmpty) + r.slot);
         if (!__all_sync(kFull, try_wait(empty, r.phase))) {
@@ -381,8 +364,15 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         int key;
         float v[4];
         __device__ __forceinline__ void next(int hi) {
+            const float* at = src;
+            if (key + 96 < hi) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = key + 32 * e < hi ? src[(key + 32 * e) * stride] : 0.f;
+                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = *at;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = key + 32 * e < hi ? *at : 0.f;
+            }
+            src = at;
             key += kTK;
         }
         // The largest and smallest, and whether all are powers of two.
@@ -397,7 +387,7 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
             }
             big = __uint_as_float(__reduce_max_sync(kFull, hi));
             small = __uint_as_float(__reduce_min_sync(kFull, lo) + 1);
-            return (__reduce_or_sync(kFull, frac) & 0x807fffffu) == 0;
+            return __all_sync(kFull, (frac & 0x807fffffu) == 0);
         }
     };
     // mul: the rows are multiplied by their scales times inv
@@ -433,16 +423,14 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
     };
     Source k{x.kb + col, x.kb + (x.lo + row0) * p.k_l + col, kStep * p.k_l, x.lo + row0};
     Source v{x.vb + col, x.vb + (x.lo + row0) * p.v_l + col, kStep * p.v_l, x.lo + row0};
-    Prefetch pf(p, x, tid, true);
-    for (int i = 0; i < kTilesAhead; ++i) pf.next<D, true>();
     for (int j = 0; j < ahead; ++j) {
         fetch(k, raw(0, j));
         fetch(v, raw(1, j));
     }
     Ring kr{2, 0, 1}, vr{2, 0, 1};
     float run = 1.17549435e-38f;   // the reference of the values' scales
-    Scales sk{p.ks + x.b * p.ks_b + x.hk * p.ks_h, p.ks_l, x.lo + lane, {}};
-    Scales sv{p.vs + x.b * p.vs_b + x.hk * p.vs_h, p.vs_l, x.lo + lane, {}};
+    Scales sk{p.ks + x.b * p.ks_b + x.hk * p.ks_h + (x.lo + lane) * p.ks_l, p.ks_l, x.lo + lane, {}};
+    Scales sv{p.vs + x.b * p.vs_b + x.hk * p.vs_h + (x.lo + lane) * p.vs_l, p.vs_l, x.lo + lane, {}};
     sk.next(x.hi);
     sv.next(x.hi);
     int kslot = 0;
@@ -453,7 +441,6 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         for (int e = 0; e < 4; ++e) at[lane + 32 * e] = sc.v[e];
     };
     for (int j = 0; j < pl.n; ++j) {
-        pf.next<D, true>();
         // f16 has codes * 2^-15 .. 1 exactly: scales that are powers of two go into the tile
         float kbig, vbig, small;
         bool kplain = sk.survey(kbig, small);
@@ -467,7 +454,7 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         // (the place of three tiles ago: the values of two tiles ago would not be
         // in if that tile's softmax were not over)
         if (!kplain) keep(ks + kslot * kTK, sk);
-        if (tid == 0) ctrl->kref[kslot] = kplain ? kbig : 0.f, ctrl->vref[kslot] = run, ctrl->vplain[kslot] = vplain;
+        if (tid == 0) ctrl->tile[kslot] = make_float4(kplain ? kbig : 0.f, run, vplain ? 0.f : 1.f, 0.f);
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * (kKFull + kr.slot));
         kr.next();
@@ -489,43 +476,53 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
 
 // ------------------------------------------------------------ products
 
-// What one thread issues for stream s: S of its tile i, and O += P V of it.
+// All products of stream s, issued by one thread.  S and P are two buffers of 64
+// columns: Q K^T of a half is issued two halves ahead of its P V, behind the P V that
+// frees its buffer.
 template <typename TM, int D, bool kFp8>
-struct Products {
+__device__ __forceinline__ void issue(const WidePlan& pl, int s, uint32_t smem_u, uint32_t tmem, Ctrl* ctrl,
+                                      uint32_t bars) {
     using L = Lay<D>;
-    static constexpr uint32_t kIdQK = instr_desc<TM>(kTK, false), kIdPV = instr_desc<TM>(D, true);
-    const WidePlan& pl;
-    uint32_t smem_u, tmem, bars;
-    Ctrl* ctrl;
-    int s;
-
-    __device__ __forceinline__ void qk(int i) const {
-        const int j = pl.tile(s, i), nk = kFp8 || pl.two ? 2 : 3, slot = j % nk;
-        const uint64_t q = smem_desc(smem_u + (pl.two ? s : 0) * L::kTile, 16);
-        const uint64_t k = smem_desc(smem_u + (slot < 2 ? 2 + slot : 1) * L::kTile, 16);
+    constexpr uint32_t kIdQK = instr_desc<TM>(kHK, false), kIdPV = instr_desc<TM>(D, true);
+    const int nk = kFp8 || pl.two ? 2 : 3, nv = kFp8 ? 2 : 3;
+    const uint64_t q = smem_desc(smem_u + (pl.two ? s : 0) * L::kTile, 16);
+    const uint32_t tS = tmem + s * kTK, tO = tmem + 2 * kTK + s * D;
+    auto qk = [&](const Halves& h) {
+        const int j = h.tile(), slot = j % nk;
+        const uint64_t k = smem_desc(smem_u + (slot < 2 ? 2 + slot : 1) * L::kTile + h.half * kHK * 128, 16);
         wait(bars + 8 * (kKFull + slot), (uint32_t)(j / nk) & 1u, &ctrl->dead);
         tc_after();
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {   // (descriptors count in 16 bytes)
             const uint32_t off = ((u >> 2) * L::kBlock + (u & 3) * 32) >> 4;
-            mma_ss(tmem + s * kTK, q + off, k + off, kIdQK, u > 0);
+            mma_ss(tS + (h.seq & 1) * kHK, q + off, k + off, kIdQK, u > 0);
         }
-        tc_commit(bars + 8 * (kSFull + s));
-        tc_commit(bars + 8 * (kKEmpty + slot));
-    }
-    __device__ __forceinline__ void pv(int i) const {
-        const int j = pl.tile(s, i), nv = kFp8 ? 2 : 3, slot = j % nv;
-        const uint64_t v = smem_desc(smem_u + (4 + slot) * L::kTile, L::kBlock);
+        tc_commit(bars + 8 * (kSFull + 2 * s + (h.seq & 1)));
+        if (h.ends_tile()) tc_commit(bars + 8 * (kKEmpty + slot));
+    };
+    auto pv = [&](const Halves& h) {
+        const int j = h.tile(), slot = j % nv;
+        const uint64_t v = smem_desc(smem_u + (4 + slot) * L::kTile + h.half * kHK * 128, L::kBlock);
         wait(bars + 8 * (kVFull + slot), (uint32_t)(j / nv) & 1u, &ctrl->dead);
-        wait(bars + 8 * (kPFull + s), (uint32_t)i & 1u, &ctrl->dead);
+        wait(bars + 8 * (kPFull + 2 * s + (h.seq & 1)), (uint32_t)(h.seq >> 1) & 1u, &ctrl->dead);
         tc_after();
 #pragma unroll
-        for (int u = 0; u < kTK / 16; ++u)
-            mma_ts(tmem + 2 * kTK + s * D, tmem + s * kTK + u * 8, v + (u * 2048 >> 4), kIdPV, i > 0 || u > 0);
-        tc_commit(bars + 8 * (kVEmpty + slot));
-        if (i == pl.count(s) - 1) tc_commit(bars + 8 * (kOFull + s));
+        for (int u = 0; u < kHK / 16; ++u)
+            mma_ts(tO, tS + (h.seq & 1) * kHK + u * 8, v + (u * 2048 >> 4), kIdPV, h.seq > 0 || u > 0);
+        tc_commit(bars + 8 * (kODone + s));
+        if (h.ends_tile()) tc_commit(bars + 8 * (kVEmpty + slot));
+    };
+    Halves a(pl, s), b(pl, s);   // of Q K^T and of P V
+    wait(bars + 8 * kQFull, 0, &ctrl->dead);
+    for (int e = 0; e < 2 && a.more(); ++e, a.next()) qk(a);
+    for (; b.more(); b.next()) {
+        pv(b);
+        if (a.more()) {
+            qk(a);
+            a.next();
+        }
     }
-};
+}
 
 // ------------------------------------------------------------ queries
 
@@ -569,194 +566,169 @@ __device__ __forceinline__ void load_query(const char* src, unsigned char* tile,
 
 // ------------------------------------------------------------ softmax
 
-// A row's running state: reference (log2 units), sum of weights, by how much the
-// reference is to rise before the next tile, and e4m3: the values' scale that O is
-// relative to.
+// A row's running state: reference (log2 units), sum of weights, and e4m3: the
+// values' scale that O is relative to.
 struct RowSum {
-    float m, l, rise, vref;
+    float m, l, vref;
 };
-// Weights are watched as the largest sum of 4 of them.  A new reference lies
-// kLow below the maximum.  Past kSoft it rises for the next tile, by a power of
-// two that leaves the sum at 2^kBase to 2^(kBase + 1), the largest weight at a
-// quarter of that or more: f16 weights then stay between 2^7 (which keeps 2^-24 of
+// Weights are watched as the largest sum of 4 of them.  A row's first reference
+// lies kLow below its maximum.  Where the sum is past kHigh the reference rises by
+// a power of two that leaves it at 2^kBase to 2^(kBase + 1), the largest weight at
+// a quarter of that or more.  f16 weights so stay between 2^7 (which keeps 2^-24 of
 // the largest at f16's 11 bits) and f16's 65504, a value's scale below 2 included.
-// Past kHard the tile's weights are made again.
 template <typename TM>
 struct Bounds {
     static constexpr bool kHalf = std::is_same<TM, __half>::value;
-    static constexpr float kLow = kHalf ? 7.f : 0.f, kSoft = kHalf ? 2048.f : 1.0995116e12f;
-    static constexpr float kHard = kHalf ? 32000.f : 1e30f;
+    static constexpr float kLow = kHalf ? 7.f : 0.f, kHigh = kHalf ? 32000.f : 1.0995116e12f;
     static constexpr int kBase = kHalf ? 9 : 2;
 };
 
-// A tile's scores: where, what multiplies them, which of them the row sees.
+// The scores of a half tile: where, what multiplies them, which of them the row sees.
 struct Scores {
     uint32_t at;
     float scale;             // of the row (and of all keys of the tile)
+    bool each;               // not all are seen, or their scales differ
     const float4 *k4, *v4;   // e4m3 whose scales are not in the tiles: the keys' (or NULL), the values' (or NULL)
     float vinv;              // what the values' are multiplied by
-    uint64_t see0, see1;
+    uint64_t see;
 };
 
-// Replace the tile's scores by the scaled ones, -inf where not seen: for tiles with
-// a mask or with scales key by key, and where the scores are so large that a fused
-// difference from the reference could lie far from that of the rounded scores.
+// The largest score that the row sees, scaled.
 template <bool kFp8>
-__device__ __forceinline__ void scale_scores(Scores& x) {
-#pragma unroll 1
-    for (int c = 0; c < kTK; c += 32) {
-        float f[32];
-        tm_ld32(x.at + c, f);
-        const uint32_t see = (uint32_t)((c < 64 ? x.see0 : x.see1) >> (c & 63));
-#pragma unroll
-        for (int u = 0; u < 32; u += 4) {
-            float k[4] = {x.scale, x.scale, x.scale, x.scale};
-            if (kFp8 && x.k4) {
-                const float4 s = x.k4[(c + u) / 4];
-                k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[u + e] = see >> (u + e) & 1 ? f[u + e] * k[e] : -INFINITY;
-        }
-        tm_put32(x.at + c, f);
-    }
-    tm_wait_st();
-    x.scale = 1.f;
-}
-
-// The largest score, scaled.
 __device__ __forceinline__ float softmax_top(const Scores& x) {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < kTK; c += 32) {
+    for (int c = 0; c < kHK; c += 32) {
         float f[32];
         tm_ld32(x.at + c, f);
+        const uint32_t see = (uint32_t)(x.see >> c);
 #pragma unroll
-        for (int u = 0; u < 32; u += 4) top = fmaxf(fmaxf(top, fmaxf(f[u], f[u + 1])), fmaxf(f[u + 2], f[u + 3]));
-    }
-    return top == -INFINITY ? top : top * x.scale;
-}
-
-// Weights relative to ref, as 16-bit pairs, and their sums: `sum` of all, `top` the
-// largest of 4.  kValue: the weights are multiplied by the values' scales.
-template <typename TM, bool kValue>
-__device__ __forceinline__ void weights32(const Scores& x, int c, float (&f)[32], uint64_t scale2, uint64_t ref2,
-                                          uint64_t (&sum)[4], float& top, uint32_t* w) {
-    // in steps over all 32, so that each step's latencies overlap
-    uint64_t a[16], t[4];
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        a[u] = ref2;
-        fma2(a[u], pack2f(f[2 * u], f[2 * u + 1]), scale2);
-    }
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        float e0, e1;
-        unpack2f(a[u], e0, e1);
-        a[u] = pack2f(ex2(e0), ex2(e1));
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        t[u] = a[u];
-#pragma unroll
-        for (int h = 4; h < 16; h += 4) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t[u]) : "l"(a[u + h]));
-        float t0, t1;
-        unpack2f(t[u], t0, t1);
-        top = fmaxf(top, fmaxf(t0, t1));
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[u]) : "l"(t[u]));
-    }
-    if (kValue) {
-#pragma unroll
-        for (int u = 0; u < 16; u += 2) {
-            const float4 v = x.v4[c / 4 + u / 2];
-            mul2(a[u], pack2f(v.x * x.vinv, v.y * x.vinv));
-            mul2(a[u + 1], pack2f(v.z * x.vinv, v.w * x.vinv));
+        for (int u = 0; u < 32; ++u) {
+            const float k = kFp8 && x.k4 ? x.scale * reinterpret_cast<const float*>(x.k4)[c + u] : x.scale;
+            top = fmaxf(top, see >> u & 1 ? f[u] * k : -INFINITY);
         }
     }
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        float e0, e1;
-        unpack2f(a[u], e0, e1);
-        w[u] = Mma<TM>::pack(e0, e1);
-    }
-}
-template <typename TM, bool kValue>
-__device__ __forceinline__ float softmax_pass(const Scores& x, float ref, float& top, uint32_t* w) {
-    const uint64_t scale2 = pack2f(x.scale, x.scale), ref2 = pack2f(-ref, -ref);
-    uint64_t sum[4] = {0, 0, 0, 0};
-    float fa[32], fb[32];
-    top = 0.f;
-    tm_get32(x.at, fa);
-#pragma unroll
-    for (int c = 0; c < kTK; c += 64) {
-        tm_wait32(fa);
-        tm_get32(x.at + c + 32, fb);
-        weights32<TM, kValue>(x, c, fa, scale2, ref2, sum, top, w + c / 2);
-        tm_wait32(fb);
-        if (c == 0) tm_get32(x.at + 64, fa);
-        weights32<TM, kValue>(x, c + 32, fb, scale2, ref2, sum, top, w + c / 2 + 16);
-    }
-    float s[8];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) unpack2f(sum[u], s[2 * u], s[2 * u + 1]);
-    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    return top;
 }
 
-// S of one tile -> P over it.  The weights are taken relative to the reference
-// that the earlier tiles left, in one pass over S; where they turn out too large
-// (hardly ever) or the row has no reference yet, the maximum is looked up, the
-// reference moves and the pass is made again.
+// S of a half tile -> P over it, in one pass over registers.  A row's first weights
+// are relative to 0: the maximum is then looked up and the pass made again, as it
+// is where weights leave fp32's range.
 template <typename TM, int D, bool kFp8>
-__device__ __forceinline__ void softmax_tile(Scores x, uint32_t tO, float vref, bool scaled, bool first, RowSum& st) {
+__device__ __forceinline__ void softmax_half(const Scores& x, uint32_t tO, float vref, uint32_t o_done, int seq,
+                                             volatile int* dead, RowSum& st) {
     using Bd = Bounds<TM>;
-    uint32_t w[kTK / 2];
-    float l, top, down = 1.f;
-    if (st.rise > 0.f) st.m += st.rise, down = ex2(-st.rise);
-    if (scaled) scale_scores<kFp8>(x);
-    bool move = st.m == -INFINITY, moved = false;
+    float f[64];
+    float (&fa)[32] = *reinterpret_cast<float (*)[32]>(f), (&fb)[32] = *reinterpret_cast<float (*)[32]>(f + 32);
+    float down = 1.f, l, top;
+    bool sought = false;
     for (;;) {
-        if (__any_sync(kFull, move)) {
-            const float next = softmax_top(x) - Bd::kLow;
-            if (move && next != -INFINITY) {
-                down *= ex2(st.m - next);   // 0 at first
+        tm_get32(x.at, fa);
+        tm_get32(x.at + 32, fb);
+        const float ref = st.m == -INFINITY ? 0.f : st.m;
+        tm_wait32(fa);
+        tm_wait32(fb);
+        float scale = x.scale;
+        if (x.each) {
+#pragma unroll
+            for (int u = 0; u < 64; u += 4) {
+                float k[4] = {scale, scale, scale, scale};
+                if (kFp8 && x.k4) {
+                    const float4 s = x.k4[u / 4];
+                    k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[u + e] = (uint32_t)(x.see >> (u & 32)) >> (u + e & 31) & 1 ? f[u + e] * k[e] : -INFINITY;
+            }
+            scale = 1.f;
+        }
+        const uint64_t scale2 = pack2f(scale, scale), ref2 = pack2f(-ref, -ref);
+        uint64_t sum[4] = {0, 0, 0, 0};
+        top = 0.f;
+        // in steps over 32, so that each step's latencies overlap
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+            for (int u = c; u < c + 32; u += 2) {
+                uint64_t a = ref2;
+                fma2(a, pack2f(f[u], f[u + 1]), scale2);
+                unpack2f(a, f[u], f[u + 1]);
+            }
+#pragma unroll
+            for (int u = c; u < c + 32; ++u) f[u] = ex2(f[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint64_t t = pack2f(f[c + 2 * u], f[c + 2 * u + 1]);
+#pragma unroll
+                for (int h = 8; h < 32; h += 8)
+                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(pack2f(f[c + h + 2 * u], f[c + h + 2 * u + 1])));
+                float t0, t1;
+                unpack2f(t, t0, t1);
+                top = fmaxf(top, fmaxf(t0, t1));
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[u]) : "l"(t));
+            }
+        }
+        float s[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) unpack2f(sum[u], s[2 * u], s[2 * u + 1]);
+        l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        if (!__any_sync(kFull, top > Bd::kHigh || st.m == -INFINITY)) break;
+        const bool seek = (top == INFINITY || st.m == -INFINITY) && !sought;
+        if (!__any_sync(kFull, seek)) {
+            float back = 1.f;
+            if (top > Bd::kHigh && top != INFINITY) {
+                // (past 2^24 the reference has steps above 1: by one at least)
+                const float rise = (float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase);
+                const float next = ref + fmaxf(rise, fabsf(ref) * 1.8e-7f);
+                back = ex2(ref - next);
                 st.m = next;
             }
-            moved = moved || move;   // once: past 2^26 the reference has no finer steps
+#pragma unroll
+            for (int u = 0; u < 64; ++u) f[u] *= back;
+            l *= back;
+            down *= back;
+            break;
         }
-        const float ref = st.m == -INFINITY ? 0.f : st.m;
-        if (!scaled && __any_sync(kFull, fabsf(ref) > 4194304.f)) {
-            scale_scores<kFp8>(x);
-            scaled = true;
+        float mx = softmax_top<kFp8>(x);
+        if (seek && mx != -INFINITY) {
+            const float next = mx - Bd::kLow;
+            down = ex2(st.m - next);   // 0 at first
+            st.m = next;
         }
-        if (kFp8 && x.v4)
-            l = softmax_pass<TM, true>(x, ref, top, w);
-        else
-            l = softmax_pass<TM, false>(x, ref, top, w);
-        move = top > Bd::kHard && !moved;
-        if (!__any_sync(kFull, move)) break;
+        sought = true;
     }
-    st.rise = top > Bd::kSoft ? (float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase) : 0.f;
     st.l = st.l * down + l;
     if constexpr (kFp8) {
-        down *= st.vref * pow2_inverse(vref);
-        st.vref = vref;
-    }
-    if (!first && __any_sync(kFull, down != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            float f[32];
-            tm_ld32(tO + c, f);
+        if (vref != st.vref) {
+            down *= st.vref * pow2_inverse(vref);
+            st.vref = vref;
+        }
+        if (x.v4) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] *= down;
-            tm_put32(tO + c, f);
+            for (int u = 0; u < 64; u += 4) {
+                const float4 v = x.v4[u / 4];
+                f[u] *= v.x * x.vinv, f[u + 1] *= v.y * x.vinv, f[u + 2] *= v.z * x.vinv, f[u + 3] *= v.w * x.vinv;
+            }
         }
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float f[32];
+    for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(Mma<TM>::pack(f[2 * u], f[2 * u + 1]));
+    tm_put32(x.at, fa);
+    if (seq > 0 && __any_sync(kFull, down != 1.f)) {
+        wait(o_done, (uint32_t)(seq - 1) & 1u, dead);   // P V of the half before is in
+        tc_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+            tm_get32(tO + c, fa);
+            tm_get32(tO + c + 32, fb);
+            tm_wait32(fa);
+            tm_wait32(fb);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(w[32 * c + e]);
-        tm_put32(x.at + 32 * c, f);
+            for (int u = 0; u < 64; ++u) f[u] *= down;
+            tm_put32(tO + c, fa);
+            tm_put32(tO + c + 32, fb);
+        }
     }
     tm_wait_st();
 }
@@ -781,13 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     pdl_wait();
     pdl_release();
 
-    const int r = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - r * p.row_tiles) * 256, rows = p.T * p.G;
-    Shard x = shard_of(p, r, blockIdx.y, blockIdx.z);
+    const int block = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - block * p.row_tiles) * 256, rows = p.T * p.G;
+    const int r = p.r0 + block;
+    const Shard x = shard_of(p, r, blockIdx.y, blockIdx.z);
     WidePlan pl;
     const int last_row = min(rows, x.live * p.G);   // rows from here on are dead
     pl.two = last_row - row0 > 128;
-    pl.cached = last_row > row0 ? (x.hi - x.lo + kTK - 1) / kTK : 0;
-    pl.n = pl.cached + (p.fold && r == p.R - 1 && last_row > row0 ? 1 : 0);
+    pl.cached = last_row > row0 && !x.drafts ? (x.hi - x.lo + kTK - 1) / kTK : 0;
+    pl.n = pl.cached + (last_row > row0 && (x.drafts || (p.fold && r == p.R - 1)) ? 1 : 0);
+    pl.len = x.hi - x.lo, pl.live = x.live;
     // the scales' rings: keys' by tile, values' by slot
     float* ks = reinterpret_cast<float*>(smem + L::kCtrl + 256);
     float* vs = ks + 3 * kTK;
@@ -801,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             init(kKFull + i, kLoadWarps), init(kKEmpty + i, users);
             init(kVFull + i, kLoadWarps), init(kVEmpty + i, users);
         }
-        for (int s = 0; s < 2; ++s) init(kSFull + s, 1), init(kPFull + s, 4), init(kOFull + s, 1);
-        init(kStart, 4);
+        for (int i = 0; i < 4; ++i) init(kSFull + i, 1), init(kPFull + i, 4);
+        for (int s = 0; s < 2; ++s) init(kODone + s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ctrl->dead = (smem_u & 1023u) != 0;   // the swizzle's atoms are 1024 bytes
         ctrl->bad = 0;
@@ -815,9 +789,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     const int s = warp >> 2 & 1;                        // softmax warps: the stream
     const int row = row0 + (pl.two ? 128 * s : 0) + (tid & 127);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's lanes of TMEM
-    RowSum st{-INFINITY, 0.f, 0.f, 1.17549435e-38f};
+    RowSum st{-INFINITY, 0.f, 1.17549435e-38f};
     uint64_t word = 0;
 
+    if (warp >= 8 + kLoadWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp < 10 + kLoadWarps && elect()) issue<TM, D, kFp8>(pl, warp - 8 - kLoadWarps, smem_u, tmem, ctrl, bars);
+        return;
+    }
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         if constexpr (kFp8)
@@ -833,76 +812,56 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             const char* src = row < last_row ? q_row(p, x.b, x.hk, row) : nullptr;
             load_query<T, D, kFp8>(src, pl.two || s == 0 ? smem + (pl.two ? s : 0) * L::kTile : nullptr, tid & 127,
                                    p.scale_log2 < 0.f, scale);
-            if (p.fold && src) word = (uint64_t)p.tree[x.b * p.tree_b + row / p.G];
+            if ((p.fold || x.drafts) && src) word = (uint64_t)p.tree[x.b * p.tree_b + row / p.G];
         }
         fence_async();
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * kQFull);
         const bool idle = row - lane >= last_row;   // no live row in the warp
         const uint32_t tS = tmem + lanes + s * kTK, tO = tmem + lanes + 2 * kTK + s * D;
-        const Products<TM, D, kFp8> products{pl, smem_u, tmem, bars, ctrl, s};
-        const bool issues = (warp & 3) == 0;
-        const int count = pl.count(s);
-        Ring vr{2, pl.two ? 0 : s, 0};
-        int kslot = pl.two ? 0 : s;
-        if (issues && count > 0 && elect()) {
-            wait(bars + 8 * kQFull, 0, &ctrl->dead);
-            if (s == 1) wait(bars + 8 * kStart, 0, &ctrl->dead);
-            products.qk(0);
-        }
-        __syncwarp();
-        for (int i = 0; i < count; ++i) {
-            const int j = pl.tile(s, i);
-            const int nkeys = j < pl.cached ? min(kTK, x.hi - x.lo - j * kTK) : x.live;
-            const bool masked = nkeys < kTK;
-            // the keys of the tile that the row sees (a masked tile's)
-            uint64_t see0 = nkeys >= 64 ? ~0ull : (1ull << nkeys) - 1;
-            uint64_t see1 = nkeys >= 128 ? ~0ull : nkeys > 64 ? (1ull << (nkeys - 64)) - 1 : 0;
-            if (j >= pl.cached) see0 &= word;
-            wait(bars + 8 * (kSFull + s), (uint32_t)i & 1u, &ctrl->dead);
-            tc_after();
-            if (!idle) {
-                Scores sc{tS, scale, nullptr, nullptr, 0.f, see0, see1};
-                float vref = 1.f;
-                bool scaled = masked;
-                if constexpr (kFp8) {
-                    const float kref = ctrl->kref[kslot];
-                    vref = ctrl->vref[kslot];
-                    if (kref != 0.f)
-                        sc.scale *= kref;
-                    else
-                        sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK);
-                    if (!ctrl->vplain[kslot]) {
-                        wait(bars + 8 * (kVFull + vr.slot), vr.phase, &ctrl->dead);   // the values' scales
-                        sc.v4 = reinterpret_cast<const float4*>(vs + vr.slot * kTK);
-                        sc.vinv = pow2_inverse(vref);
-                    }
-                    scaled = scaled || sc.k4;
-                    __syncwarp();
+        int seq = 0;
+        for (int i = 0; i < pl.count(s); ++i) {
+            const int j = pl.tile(s, i), keys = pl.keys(j), kslot = j % 3;
+#pragma unroll 1
+            for (int half = 0; half < 2 && half * kHK < keys; ++half, ++seq) {
+                const int left = keys - half * kHK, buf = seq & 1;
+                Scores sc{tS + buf * kHK, scale, left < kHK || j >= pl.cached, nullptr, nullptr, 0.f, ~0ull};
+                if (sc.each) {
+                    if (left < kHK) sc.see = (1ull << left) - 1;
+                    if (j >= pl.cached) sc.see &= word;
                 }
-                softmax_tile<TM, D, kFp8>(sc, tO, vref, scaled, i == 0, st);
+                wait(bars + 8 * (kSFull + 2 * s + buf), (uint32_t)(seq >> 1) & 1u, &ctrl->dead);
+                tc_after();
+                if (!idle) {
+                    float vref = 1.f;
+                    if constexpr (kFp8) {
+                        const float4 t = ctrl->tile[kslot];
+                        vref = t.y;
+                        sc.scale *= t.x;
+                        if (t.x == 0.f) {
+                            sc.scale = scale;
+                            sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK + half * kHK);
+                            sc.each = true;
+                        }
+                        if (t.z != 0.f) {
+                            wait(bars + 8 * (kVFull + j % 2), (uint32_t)(j / 2) & 1u, &ctrl->dead);   // their scales
+                            sc.v4 = reinterpret_cast<const float4*>(vs + j % 2 * kTK + half * kHK);
+                            sc.vinv = pow2_inverse(vref);
+                            __syncwarp();
+                        }
+                    }
+                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + s), seq, &ctrl->dead, st);
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) arrive(bars + 8 * (kPFull + 2 * s + buf));
             }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) {
-                arrive(bars + 8 * (kPFull + s));
-                if (s == 0 && i == 0) arrive(bars + 8 * kStart);
-            }
-            if (issues && elect()) {
-                products.pv(i);
-                if (i + 1 < count) products.qk(i + 1);
-            }
-            __syncwarp();
-            // ring places of the stream's next tile
-            vr.next();
-            if (!pl.two) vr.next();
-            kslot += pl.two ? 1 : 2;
-            if (kslot >= 3) kslot -= 3;
         }
-        if (count > 0) wait(bars + 8 * (kOFull + s), 0, &ctrl->dead);
+        const int last = seq - 1;   // the last P V
+        if (last >= 0) wait(bars + 8 * (kODone + s), (uint32_t)last & 1u, &ctrl->dead);
         if (ctrl->dead) {   // what was issued has to be complete before TMEM is freed
             const int64_t t0 = clock64();
-            while (count > 0 && !try_wait(bars + 8 * (kOFull + s), 0) && clock64() - t0 < kGiveUpClocks) {
+            while (last >= 0 && !try_wait(bars + 8 * (kODone + s), (uint32_t)last & 1u) && clock64() - t0 < kGiveUpClocks) {
             }
         }
         tc_after();
@@ -954,10 +913,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         const bool store = row < rows;
         char* dst;
         int kind = p.out_dtype;
-        if (p.po) {
-            dst = reinterpret_cast<char*>(p.po + (at * p.shards + r) * D);
+        // the drafts' shard, written by an earlier launch, joins the only other one here
+        const float* joined = nullptr;
+        float b0 = 1.f, b1 = 0.f;
+        if (p.join && store) {
+            joined = p.po + at * D;
+            const float l1 = __ldcg(p.pl + at);
+            const float mx = fmaxf(lse, l1), ref = mx == -INFINITY ? 0.f : mx;
+            const float e0 = expf(lse - ref), e1 = expf(l1 - ref), total = e0 + e1;
+            const bool seen = total != 0.f;   // NaN where a score was
+            b0 = seen ? e0 / total : 0.f;
+            b1 = seen ? e1 / total : 0.f;
+            lse = seen ? mx + logf(total) : -INFINITY;
+        }
+        if (p.po && !p.join) {
+            const int64_t place = p.shards > 1 ? at * p.shards + r : at;
+            dst = reinterpret_cast<char*>(p.po + place * D);
             kind = LSE_MERGE_F32;
-            if (store) p.pl[at * p.shards + r] = lse;
+            if (store) p.pl[place] = lse;
         } else {
             dst = p.out + at * D * (int64_t)(kind == LSE_MERGE_F32 ? 4 : 2);
             if (store) p.out_lse[at] = lse;
@@ -992,6 +965,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             }
 #pragma unroll
             for (int u = 0; u < 32; ++u) f[u] = any ? f[u] * inv : 0.f;
+            if (joined) {
+#pragma unroll
+                for (int u = 0; u < 32; u += 4) {
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(joined + c * 32 + u));
+                    f[u] = f[u] * b0 + o.x * b1, f[u + 1] = f[u + 1] * b0 + o.y * b1;
+                    f[u + 2] = f[u + 2] * b0 + o.z * b1, f[u + 3] = f[u + 3] * b0 + o.w * b1;
+                }
+            }
             if (kind == LSE_MERGE_F32) {
                 float4* o = reinterpret_cast<float4*>(dst + c * 128);
 #pragma unroll
@@ -1028,8 +1009,8 @@ WideFn pick(int D, bool fp8) {
 
 }  // namespace
 
-cudaError_t launch_tree_wide(const TreeParams& p, int dtype, bool fp8, int out_dtype, int B, int Hkv, int D, bool pdl,
-                             cudaStream_t stream) {
+cudaError_t launch_tree_wide(const TreeParams& p, int dtype, bool fp8, int shards, int out_dtype, int B, int Hkv, int D,
+                             bool pdl, cudaStream_t stream) {
     const WideFn fn = dtype == LSE_MERGE_F16 ? pick<__half>(D, fp8) : pick<__nv_bfloat16>(D, fp8);
     const int smem = D == 64 ? Lay<64>::kBytes : Lay<128>::kBytes;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem);
@@ -1041,7 +1022,7 @@ cudaError_t launch_tree_wide(const TreeParams& p, int dtype, bool fp8, int out_d
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(q.row_tiles * p.R), (unsigned)Hkv, (unsigned)B);
+    cfg.gridDim = dim3((unsigned)(q.row_tiles * shards), (unsigned)Hkv, (unsigned)B);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
