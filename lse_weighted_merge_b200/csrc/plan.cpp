@@ -468,10 +468,14 @@ int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* pl
     return LSE_MERGE_OK;
 }
 
-// Shards of the cached keys.  Up to 16 query rows per KV head (rows16 kernel): enough
-// for about two CTAs per SM, a power of two of at least 64 keys each, at most 64.
-// More rows (wide kernel, one CTA per SM, tiles of 128 keys): the R that gives the
-// fewest tiles per SM, with 3 tiles' time for the start and end of a CTA.
+// Shards of the cached keys: the R with the least modelled time on `sms` SMs.  Up to
+// 16 query rows per KV head (rows16 kernel, two CTAs per SM, steps of 128 keys): a
+// CTA's start and end take about as long as 5.5 steps, two CTAs on an SM take 1.35
+// times as long as one, each shard adds to the merge.  (Measured for one sequence of
+// 4096 e4m3 tokens, 8 KV heads: R = 1, 4, 8, 16, 32, 64 in 38.7, 16.8, 12.5, 10.8,
+// 12.4, 20.8 us.)  More rows (wide kernel, one CTA per SM, tiles of 128 keys): start
+// and end take about 3 tiles' time.  (4096 bf16 tokens under 20 rows: R = 1, 4, 8,
+// 16, 32 in 54.6, 23.6, 17.5, 15.2, 22.9 us.)
 int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms) {
     if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || L < 1 || D < 1 || sms < 1) return 1;
     const int64_t rows = (int64_t)T * (Hq / Hkv);
@@ -485,8 +489,14 @@ int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms) {
         }
         return R;
     }
-    const int64_t units = (int64_t)B * Hkv;
-    while (units * R < 2 * (int64_t)sms && R < 64 && R * 64 < L) R *= 2;
+    const int64_t units = (int64_t)B * Hkv, steps = ((int64_t)L + 127) / 128;
+    double best = -1;
+    for (int r = 1; r <= 64 && r <= steps; ++r) {
+        const int64_t ctas = units * r, waves = (ctas + 2 * (int64_t)sms - 1) / (2 * (int64_t)sms);
+        const double each = 5.5 + (double)((steps + r - 1) / r);
+        const double cost = (double)waves * each * (ctas > sms ? 1.35 : 1.0) + 0.04 * r;
+        if (best < 0 || cost < best) best = cost, R = r;
+    }
     return R;
 }
 

@@ -537,32 +537,37 @@ __global__ void __launch_bounds__(kRowWarps * 32) tree_rows16_kernel(const TreeP
 
 // -------------------------------------------------------------------- merge
 
-// The LSE merge of a row's shards: D / 4 lanes per row, 4 elements each, the
-// loads of kBatch shards in flight before any is used, folded into a running
-// (max, weight sum, weighted sum).  (lse_merge gives -inf as the lse of a row
-// one of whose partials is NaN; here that is NaN.)
-template <typename TOut, int D>
+// The LSE merge of a row's shards.  D / 4 lanes hold a row, 4 elements each; kWide
+// gives a row to the whole block, whose groups of lanes take every 4th (D = 64: 8th)
+// shard and join through shared memory, else to one group.  The loads of kBatch
+// shards are in flight before any is used, folded into a running (max, weight sum,
+// weighted sum).  (lse_merge gives -inf as the lse of a row one of whose partials is
+// NaN; here that is NaN.)
+// Few rows with many shards are bound by latency: 32 rows of 16 shards and 4096 keys
+// (one decode step of one sequence) take 12.8 us with a group per row.
+template <typename TOut, int D, bool kWide>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const float* po, const float* pl, int shards, uint32_t rows,
                                                          char* out, float* out_lse) {
-    constexpr int kLanes = D / 4, kBatch = 8;
-    pdl_wait();
-    pdl_release();
-    const uint32_t row = (blockIdx.x * 128u + threadIdx.x) / kLanes;
-    const int lane = threadIdx.x % kLanes;
+    constexpr int kLanes = D / 4, kGroups = 128 / kLanes, kBatch = 8;
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const uint32_t row = kWide ? blockIdx.x : blockIdx.x * kGroups + group;
     if (row >= rows) return;
+    const int first = kWide ? group : 0, step = kWide ? kGroups : 1;
     const float* o = po + (int64_t)row * shards * D + lane * 4;
     const float* l = pl + (int64_t)row * shards;
+    pdl_wait();
+    pdl_release();
     float mx = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < shards; s0 += kBatch) {
+    for (int s0 = first; s0 < shards; s0 += kBatch * step) {
         float lv[kBatch];
         float4 ov[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const bool in = s0 + u < shards;
-            lv[u] = in ? __ldcg(l + s0 + u) : -INFINITY;
-            ov[u] = in ? __ldcg(reinterpret_cast<const float4*>(o + (int64_t)(s0 + u) * D))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            const int s = s0 + u * step;
+            const bool in = s < shards;
+            lv[u] = in ? __ldcg(l + s) : -INFINITY;
+            ov[u] = in ? __ldcg(reinterpret_cast<const float4*>(o + (int64_t)s * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float top = mx;
 #pragma unroll
@@ -582,6 +587,31 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const float* po, const 
         }
         mx = top;
     }
+    if constexpr (kWide) {
+        __shared__ float4 other[128];
+        __shared__ float2 state[kGroups];
+        other[threadIdx.x] = num;
+        if (lane == 0) state[group] = make_float2(mx, den);
+        __syncthreads();
+        if (group > 0) return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) top = fmaxf(top, state[g].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        den = 0.f;
+        num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {   // (a group that saw no key has sums 0, or NaN)
+            const float e = state[g].x == -INFINITY ? 1.f : expf(state[g].x - ref);
+            const float4 v = other[g * kLanes + lane];
+            den = fmaf(e, state[g].y, den);
+            num.x = fmaf(e, v.x, num.x);
+            num.y = fmaf(e, v.y, num.y);
+            num.z = fmaf(e, v.z, num.z);
+            num.w = fmaf(e, v.w, num.w);
+        }
+        mx = top;
+    }
     const bool any = den != 0.f;   // NaN where a partial is
     const float inv = any ? 1.f / den : 0.f;
     const float f[4] = {num.x * inv, num.y * inv, num.z * inv, num.w * inv};
@@ -596,14 +626,15 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const float* po, const 
 
 using MergeFn = void (*)(const float*, const float*, int, uint32_t, char*, float*);
 template <typename TOut>
-MergeFn pick_merge_d(int D) {
-    return D == 64 ? tree_merge_kernel<TOut, 64> : tree_merge_kernel<TOut, 128>;
+MergeFn pick_merge_d(int D, bool wide) {
+    if (D == 64) return wide ? tree_merge_kernel<TOut, 64, true> : tree_merge_kernel<TOut, 64, false>;
+    return wide ? tree_merge_kernel<TOut, 128, true> : tree_merge_kernel<TOut, 128, false>;
 }
-MergeFn pick_merge(int out_dtype, int D) {
+MergeFn pick_merge(int out_dtype, int D, bool wide) {
     switch (out_dtype) {
-        case LSE_MERGE_F32: return pick_merge_d<float>(D);
-        case LSE_MERGE_F16: return pick_merge_d<__half>(D);
-        default: return pick_merge_d<__nv_bfloat16>(D);
+        case LSE_MERGE_F32: return pick_merge_d<float>(D, wide);
+        case LSE_MERGE_F16: return pick_merge_d<__half>(D, wide);
+        default: return pick_merge_d<__nv_bfloat16>(D, wide);
     }
 }
 
@@ -736,11 +767,13 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
         }
     }
     if (e == cudaSuccess && p.shards > 1) {
-        const uint32_t rows = (uint32_t)a.B * a.T * a.Hq, per = 128u / (uint32_t)(a.D / 4);
+        // a block per row where a group's loads would come in more than one batch of 4
+        const bool spread = p.shards > 4;
+        const uint32_t rows = (uint32_t)a.B * a.T * a.Hq, per = spread ? 1u : 128u / (uint32_t)(a.D / 4);
         cfg.gridDim = dim3((rows + per - 1) / per);
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, pick_merge(a.out_dtype, a.D), (const float*)p.po, (const float*)p.pl, p.shards,
+        e = cudaLaunchKernelEx(&cfg, pick_merge(a.out_dtype, a.D, spread), (const float*)p.po, (const float*)p.pl, p.shards,
                                rows, static_cast<char*>(a.out_o), a.out_lse);
     }
     if (e != cudaSuccess) {
