@@ -19,6 +19,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "lse_merge.h"
@@ -74,16 +76,81 @@ __device__ __forceinline__ uint4 ld16(const char* p) {
                  : "l"(p));
     return v;
 }
-// The 8 elements of T at p as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const char* p, float (&f)[8]) {
-    Elem<T>::unpack(ld16(p), f);
-    if constexpr (sizeof(T) == 4) Elem<T>::unpack(ld16(p + 16), f + 4);
+__device__ __forceinline__ uint2 ld8(const char* p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
+// 16 elements of a row per lane, as two runs of 8 that lie D / 2 apart (so that a
+// load of all lanes is contiguous).
+template <typename T>
+struct Run;
+template <>
+struct Run<float> {
+    uint4 u[4];
+    __device__ __forceinline__ void load(const char* p, int apart) {
+        u[0] = ld16(p), u[1] = ld16(p + 16), u[2] = ld16(p + apart), u[3] = ld16(p + apart + 16);
+    }
+    // Bits of the largest magnitude (as integers: infinities and NaN are largest).
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            m = max(max(max(m, u[k].x & 0x7fffffffu), max(u[k].y & 0x7fffffffu, u[k].z & 0x7fffffffu)), u[k].w & 0x7fffffffu);
+        return m;
+    }
+    __device__ static uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+    __device__ static uint32_t bits(uint32_t m) { return m; }
+    __device__ __forceinline__ void get(float (&f)[16]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) Elem<float>::unpack(u[k], f + 4 * k);
+    }
+};
+// 16-bit types: two magnitudes per 32-bit word.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T>
+struct Run16 {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const char* p, int apart) { u[0] = ld16(p), u[1] = ld16(p + apart); }
+    __device__ __forceinline__ uint32_t top() const {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t a = max_u16x2(max_u16x2(u[0].x & kAbs, u[0].y & kAbs), max_u16x2(u[0].z & kAbs, u[0].w & kAbs));
+        const uint32_t b = max_u16x2(max_u16x2(u[1].x & kAbs, u[1].y & kAbs), max_u16x2(u[1].z & kAbs, u[1].w & kAbs));
+        return max_u16x2(a, b);
+    }
+    __device__ static uint32_t join(uint32_t a, uint32_t b) { return max_u16x2(a, b); }
+    // fp32 bits of the larger of the two.
+    __device__ static uint32_t bits(uint32_t m) {
+        float f[2];
+        Run16::unpack(max(m & 0xffffu, m >> 16), f);
+        return __float_as_uint(f[0]);
+    }
+    __device__ static void unpack(uint32_t w, float* f) {
+        if constexpr (std::is_same<T, __half>::value)
+            unpack_f16x2(w, f);
+        else
+            unpack_bf16x2(w, f);
+    }
+    __device__ __forceinline__ void get(float (&f)[16]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) Elem<T>::unpack(u[k], f + 8 * k);
+    }
+};
+template <>
+struct Run<__half> : Run16<__half> {};
+template <>
+struct Run<__nv_bfloat16> : Run16<__nv_bfloat16> {};
 
+// D / 16 lanes per row.  The maximum is taken over the magnitudes' bits, which is
+// also how a row with elements that are no numbers is noticed: it takes a path of
+// its own, and the others test nothing.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_quantize_kernel(const KvParams p) {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 16, E = (int)sizeof(T);
     pdl_wait();
     pdl_release();
     const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / kLanes;
@@ -94,82 +161,112 @@ __global__ void __launch_bounds__(256) kv_quantize_kernel(const KvParams p) {
     const int pos = (int)min((int64_t)p.start[b] + j, (int64_t)INT32_MAX);
     const bool there = pos >= 0 && pos < p.L && (!p.count || j < p.count[b]);
     const int src = there && p.select ? p.select[(int64_t)b * p.T + j] : j;
-    const bool live = there && src >= 0 && src < p.S;
-    if (!live) return;
+    if (!there || src < 0 || src >= p.S) return;
     const unsigned group = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
-    float f[2][8];
+    Run<T> x[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-        load8<T>(p.x[s] + b * p.x_b[s] + h * p.x_h[s] + src * p.x_t[s] + lane * 8 * (int)sizeof(T), f[s]);
+        x[s].load(p.x[s] + b * p.x_b[s] + h * p.x_h[s] + src * p.x_t[s] + lane * 8 * E, D / 2 * E);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        float a = 0.f;
+        uint32_t m = x[s].top();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float m = fabsf(f[s][k]);
-            const bool fin = m <= 3.402823466e38f;
-            f[s][k] = fin ? f[s][k] : __uint_as_float(0x7fc00000u);
-            a = fin ? fmaxf(a, m) : a;
+        for (int o = kLanes / 2; o; o >>= 1) m = Run<T>::join(m, __shfl_xor_sync(group, m, o));
+        uint32_t bits = Run<T>::bits(m);
+        float f[16];
+        x[s].get(f);
+        if (bits >= 0x7f800000u) {
+            float a = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float v = fabsf(f[k]);
+                const bool fin = v <= 3.402823466e38f;
+                f[k] = fin ? f[k] : __uint_as_float(0x7fc00000u);
+                a = fin ? fmaxf(a, v) : a;
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+            bits = __float_as_uint(a);
         }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
-        const uint32_t bits = __float_as_uint(a);
         int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
         e = max(e, -126);
         if (bits == 0) e = 0;
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        uint2 w;
-        w.x = to_e4m3x2(f[s][0] * inv, f[s][1] * inv) | to_e4m3x2(f[s][2] * inv, f[s][3] * inv) << 16;
-        w.y = to_e4m3x2(f[s][4] * inv, f[s][5] * inv) | to_e4m3x2(f[s][6] * inv, f[s][7] * inv) << 16;
-        *reinterpret_cast<uint2*>(p.cache[s] + b * p.c_b[s] + h * p.c_h[s] + pos * p.c_l[s] + lane * 8) = w;
+        char* to = p.cache[s] + b * p.c_b[s] + h * p.c_h[s] + pos * p.c_l[s] + lane * 8;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float* g = f + 8 * r;
+            uint2 w;
+            w.x = to_e4m3x2(g[0] * inv, g[1] * inv) | to_e4m3x2(g[2] * inv, g[3] * inv) << 16;
+            w.y = to_e4m3x2(g[4] * inv, g[5] * inv) | to_e4m3x2(g[6] * inv, g[7] * inv) << 16;
+            *reinterpret_cast<uint2*>(to + r * (D / 2)) = w;
+        }
         if (lane == 0)
             p.scale[s][b * p.s_b[s] + h * p.s_h[s] + pos * p.s_l[s]] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(256) kv_dequantize_kernel(const KvParams p) {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
     pdl_wait();
     pdl_release();
-    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
-    if (i >= p.rows) return;
-    int b, h, j;
-    row_of(p, i, b, h, j);
-    const int pos = (int)min((int64_t)p.start[b] + j, (int64_t)INT32_MAX);
-    const bool there = pos >= 0 && pos < p.L && (!p.count || j < p.count[b]);
+    uint2 w[U][2];
+    float sc[U][2];
+    int64_t to[U][2];
+    bool in[U];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (there) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p.cache[s] + b * p.c_b[s] + h * p.c_h[s] +
-                                                            pos * p.c_l[s] + lane * 8);
-            const float sc = p.scale[s][b * p.s_b[s] + h * p.s_h[s] + pos * p.s_l[s]];
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = (blockIdx.x * U + u) * kGroups + threadIdx.x / kLanes;
+        in[u] = i < p.rows;
+        int b, h, j;
+        row_of(p, min(i, p.rows - 1), b, h, j);
+        const int pos = (int)min((int64_t)p.start[b] + j, (int64_t)INT32_MAX);
+        const bool there = in[u] && pos >= 0 && pos < p.L && (!p.count || j < p.count[b]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 v = from_e4m3x2((k < 2 ? w.x : w.y) >> (16 * (k & 1)) & 0xffffu);
-                f[2 * k] = v.x * sc;
-                f[2 * k + 1] = v.y * sc;
+        for (int s = 0; s < 2; ++s) {
+            w[u][s] = make_uint2(0u, 0u);
+            sc[u][s] = 0.f;
+            to[u][s] = b * p.x_b[s] + h * p.x_h[s] + j * p.x_t[s];
+            if (there) {
+                w[u][s] = ld8(p.cache[s] + b * p.c_b[s] + h * p.c_h[s] + pos * p.c_l[s] + lane * 8);
+                sc[u][s] = p.scale[s][b * p.s_b[s] + h * p.s_h[s] + pos * p.s_l[s]];
             }
         }
-        store_vec<T, 8>(p.x[s] + b * p.x_b[s] + h * p.x_h[s] + j * p.x_t[s] + lane * 8 * (int)sizeof(T), f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (!in[u]) continue;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 v = from_e4m3x2((k < 2 ? w[u][s].x : w[u][s].y) >> (16 * (k & 1)) & 0xffffu);
+                f[2 * k] = v.x * sc[u][s];
+                f[2 * k + 1] = v.y * sc[u][s];
+            }
+            store_vec<T, 8>(p.x[s] + to[u][s] + lane * 8 * (int)sizeof(T), f);
+        }
     }
 }
 
 using KvFn = void (*)(KvParams);
 
-template <typename T>
-KvFn pick_d(bool write, int D) {
-    if (write) return D == 64 ? kv_quantize_kernel<T, 64> : kv_quantize_kernel<T, 128>;
-    return D == 64 ? kv_dequantize_kernel<T, 64> : kv_dequantize_kernel<T, 128>;
-}
+constexpr int kManyRows = 2;   // rows read back per group of lanes where there are many
 
-KvFn pick(bool write, int dtype, int D) {
+template <typename T>
+KvFn pick_d(bool write, bool many, int D) {
+    if (write) return D == 64 ? kv_quantize_kernel<T, 64> : kv_quantize_kernel<T, 128>;
+    if (many) return D == 64 ? kv_dequantize_kernel<T, 64, kManyRows> : kv_dequantize_kernel<T, 128, kManyRows>;
+    return D == 64 ? kv_dequantize_kernel<T, 64, 1> : kv_dequantize_kernel<T, 128, 1>;
+}
+KvFn pick(bool write, bool many, int dtype, int D) {
     switch (dtype) {
-        case LSE_MERGE_F32: return pick_d<float>(write, D);
-        case LSE_MERGE_F16: return pick_d<__half>(write, D);
-        default: return pick_d<__nv_bfloat16>(write, D);
+        case LSE_MERGE_F32: return pick_d<float>(write, many, D);
+        case LSE_MERGE_F16: return pick_d<__half>(write, many, D);
+        default: return pick_d<__nv_bfloat16>(write, many, D);
     }
 }
 
@@ -206,7 +303,9 @@ int launch(const lse_merge_kv_args* args, bool write, cudaStream_t stream) {
     p.div0 = fastdiv_c(p.n0);
     p.div1 = fastdiv_c(p.n1);
     p.rows = (uint32_t)a.B * p.n0 * p.n1;
-    const uint32_t per = 256u / (uint32_t)(a.D / 8);
+    // (many: one row each would still fill the GPU's 148 x 2048 threads twice over)
+    const bool many = !write && (int64_t)p.rows * (a.D / 8) > 2 * kManyRows * 148 * 2048;
+    const uint32_t per = write ? 256u / (uint32_t)(a.D / 16) : 256u / (uint32_t)(a.D / 8) * (many ? kManyRows : 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.rows + per - 1) / per);
     cfg.blockDim = dim3(256);
@@ -216,7 +315,7 @@ int launch(const lse_merge_kv_args* args, bool write, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPdl ? 1 : 0;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, pick(write, a.dtype, a.D), p);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, pick(write, many, a.dtype, a.D), p);
     if (err != cudaSuccess) {
         set_last_cuda_error((int)err);
         (void)cudaGetLastError();
