@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kRowWarps = 4;
 constexpr int kRowStages = 3;
+constexpr int kRowCtas = 2;     // per SM
 
 // The running state of a warp's online softmax: rows g and g + 8, log2 units.
 template <int D>
@@ -63,53 +64,74 @@ struct RowState {
     }
 };
 
+// The reference of a row's weights lies kLow below the maximum when it is set, and
+// is moved when a score lies kHigh above it (the o of all rows is scaled then, so it
+// is done seldom).  With f16 weights 2^7 .. 2^14 is the largest one's range: those
+// down to 2^-21 of it at least keep f16's 11 bits, and times a value's scale below 2
+// they stay below f16's 65504.  bf16 has fp32's range.
+template <typename TM>
+struct Reference {
+    static constexpr bool kHalf = std::is_same<TM, __half>::value;
+    static constexpr float kLow = kHalf ? 7.f : 0.f, kHigh = kHalf ? 14.f : 30.f;
+};
+__device__ __forceinline__ float ex2(float x) {   // results below 2^-126 are 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Fold the tile's scores (C layout, log2 units, -inf where not seen) into the
-// running maxima and sums: on return sc holds the weights exp2(s - reference),
-// the reference kBias below the maximum.  A row without any key so far keeps
-// m = -inf, sums 0.
-template <int D, int NJ, int kBias>
+// running sums: on return sc holds the weights exp2(s - reference).  A row without
+// any key so far keeps m = -inf, sums 0.  kRows8: there are no rows g + 8.
+template <typename TM, int D, int NJ, bool kRows8>
 __device__ __forceinline__ void softmax_step(float (&sc)[NJ][4], RowState<D>& w) {
-    float mx0 = w.m0, mx1 = w.m1;
+    using Ref = Reference<TM>;
+    float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][1]) - kBias);
-        mx1 = fmaxf(mx1, fmaxf(sc[j][2], sc[j][3]) - kBias);
+        mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][1]));
+        if (!kRows8) mx1 = fmaxf(mx1, fmaxf(sc[j][2], sc[j][3]));
     }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 2));
-    const float r0 = mx0 == -INFINITY ? 0.f : mx0, r1 = mx1 == -INFINITY ? 0.f : mx1;
-    const float a0 = exp2f(w.m0 - r0), a1 = exp2f(w.m1 - r1);
-    w.m0 = mx0;
-    w.m1 = mx1;
-    w.l0 *= a0;
-    w.l1 *= a1;
+    bool move = mx0 - w.m0 > Ref::kHigh;   // (of any lane of the row: NaN, no key, is false)
+    if (!kRows8) move = move || mx1 - w.m1 > Ref::kHigh;
+    if (__any_sync(kFull, move)) {
+        auto raise = [](float mx, float& m, float& l) {
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            if (!(mx - m > Ref::kHigh)) return 1.f;
+            const float next = mx - Ref::kLow, a = ex2(m - next);   // 0 at first
+            m = next;
+            l *= a;
+            return a;
+        };
+        const float a0 = raise(mx0, w.m0, w.l0);
+        float a1 = 1.f;
+        if (!kRows8) a1 = raise(mx1, w.m1, w.l1);
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        w.o[n][0] *= a0;
-        w.o[n][1] *= a0;
-        w.o[n][2] *= a1;
-        w.o[n][3] *= a1;
+        for (int n = 0; n < D / 8; ++n) {
+            w.o[n][0] *= a0;
+            w.o[n][1] *= a0;
+            if (!kRows8) w.o[n][2] *= a1, w.o[n][3] *= a1;
+        }
     }
+    const float r0 = w.m0 == -INFINITY ? 0.f : w.m0, r1 = w.m1 == -INFINITY ? 0.f : w.m1;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        sc[j][0] = exp2f(sc[j][0] - r0);
-        sc[j][1] = exp2f(sc[j][1] - r0);
-        sc[j][2] = exp2f(sc[j][2] - r1);
-        sc[j][3] = exp2f(sc[j][3] - r1);
+        sc[j][0] = ex2(sc[j][0] - r0);
+        sc[j][1] = ex2(sc[j][1] - r0);
         w.l0 += sc[j][0] + sc[j][1];
-        w.l1 += sc[j][2] + sc[j][3];
+        if (!kRows8) {
+            sc[j][2] = ex2(sc[j][2] - r1);
+            sc[j][3] = ex2(sc[j][3] - r1);
+            w.l1 += sc[j][2] + sc[j][3];
+        }
     }
 }
 
 // ------------------------------------------------------------ 16-bit tiles
 
-template <typename T>
-constexpr int kWeightBias = std::is_same<T, __half>::value ? 10 : 0;   // see the head of the file
-
 // Tiles of 16 keys, K then V, rows of 2 * D bytes swizzled by tile_off.
-template <typename T, int D>
+template <typename T, int D, bool kRows8>
 struct Tiles16 {
     static constexpr int TK = 16;
     static constexpr int kBytes = 2 * TK * D * 2;
@@ -173,14 +195,14 @@ struct Tiles16 {
                     ok1 = ok1 && (word1 >> (key & 63) & 1);
                 }
                 sc[j][e] = ok0 ? sc[j][e] * q.scale0 : -INFINITY;
-                sc[j][e + 2] = ok1 ? sc[j][e + 2] * q.scale1 : -INFINITY;
+                if (!kRows8) sc[j][e + 2] = ok1 ? sc[j][e + 2] * q.scale1 : -INFINITY;
             }
-        softmax_step<D, 2, kWeightBias<T>>(sc, w);
+        softmax_step<T, D, 2, kRows8>(sc, w);
         uint32_t pa[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             pa[2 * j] = Mma<T>::pack(sc[j][0], sc[j][1]);
-            pa[2 * j + 1] = Mma<T>::pack(sc[j][2], sc[j][3]);
+            pa[2 * j + 1] = kRows8 ? 0u : Mma<T>::pack(sc[j][2], sc[j][3]);
         }
         bool bad = false;
         if (x.drafts) {
@@ -232,7 +254,7 @@ struct Tiles16 {
 // -------------------------------------------------------------- e4m3 tiles
 
 // Tiles of 32 keys: K codes, V codes, K scales, V scales.
-template <typename T, int D>
+template <typename T, int D, bool kRows8>
 struct Tiles8 {
     static constexpr int TK = 32;
     static constexpr int kVOff = TK * D;
@@ -251,13 +273,16 @@ struct Tiles8 {
     }
 
     __device__ static void issue(const TreeParams& p, const Shard& x, int key0, uint32_t st, int lane) {
+        const char* kp = x.kb + (key0 + lane / CPR) * p.k_l + lane % CPR * 16;
+        const char* vp = x.vb + (key0 + lane / CPR) * p.v_l + lane % CPR * 16;
 #pragma unroll
         for (int i = 0; i < TK * CPR / 32; ++i) {
-            const int c = lane + 32 * i, row = c / CPR, ch = c - row * CPR;
+            const int row = lane / CPR + i * (32 / CPR), ch = lane % CPR;
             const bool ok = key0 + row < x.hi;
-            const int64_t key = ok ? key0 + row : x.lo;
-            cp_async16(st + k_off(row, ch), x.kb + key * p.k_l + ch * 16, ok ? 16 : 0);
-            cp_async16(st + kVOff + v_off(row, ch), x.vb + key * p.v_l + ch * 16, ok ? 16 : 0);
+            cp_async16(st + k_off(row, ch), ok ? kp : x.kb, ok ? 16 : 0);
+            cp_async16(st + kVOff + v_off(row, ch), ok ? vp : x.vb, ok ? 16 : 0);
+            kp += (32 / CPR) * p.k_l;
+            vp += (32 / CPR) * p.v_l;
         }
         const bool ok = key0 + lane < x.hi;
         const int64_t key = ok ? key0 + lane : x.lo;
@@ -342,10 +367,10 @@ struct Tiles8 {
                     const bool ok = key0 + 16 * kk + 4 * t + 2 * h + e < x.hi;
                     float* c = sc[2 * kk + h];
                     c[e] = ok ? c[e] * (s[2 * h + e] * q.scale0) : -INFINITY;
-                    c[e + 2] = ok ? c[e + 2] * (s[2 * h + e] * q.scale1) : -INFINITY;
+                    if (!kRows8) c[e + 2] = ok ? c[e + 2] * (s[2 * h + e] * q.scale1) : -INFINITY;
                 }
         }
-        softmax_step<D, NJ, 10>(sc, w);
+        softmax_step<__half, D, NJ, kRows8>(sc, w);
         // the reference of the values' scales: a power of two, only raised
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs[lane])));
         const float ref = fmaxf(vref, pow2_below(top));
@@ -355,8 +380,7 @@ struct Tiles8 {
             for (int n = 0; n < D / 8; ++n) {
                 w.o[n][0] *= down;
                 w.o[n][1] *= down;
-                w.o[n][2] *= down;
-                w.o[n][3] *= down;
+                if (!kRows8) w.o[n][2] *= down, w.o[n][3] *= down;
             }
             vref = ref;
         }
@@ -370,7 +394,7 @@ struct Tiles8 {
             for (int h = 0; h < 2; ++h) {
                 const float* c = sc[2 * kk + h];
                 pa[2 * h] = Mma<__half>::pack(c[0] * s[2 * h], c[1] * s[2 * h + 1]);
-                pa[2 * h + 1] = Mma<__half>::pack(c[2] * s[2 * h], c[3] * s[2 * h + 1]);
+                pa[2 * h + 1] = kRows8 ? 0u : Mma<__half>::pack(c[2] * s[2 * h], c[3] * s[2 * h + 1]);
             }
             // keys 4t .. 4t + 3 of this step at D / 8 consecutive d from g * D / 8
             uint32_t u[4][D / 32];
@@ -476,11 +500,11 @@ __device__ __forceinline__ void store_state(float* st, int warp, int lane, const
 
 // grid (row tiles * shards, Hkv, B), row tiles fastest: the tiles of a shard
 // run at the same time and share its keys through L2
-template <typename T, int D, bool kFp8, typename TOut>
-__global__ void __launch_bounds__(kRowWarps * 32) tree_rows16_kernel(const TreeParams p) {
+template <typename T, int D, bool kFp8, bool kRows8, typename TOut>
+__global__ void __launch_bounds__(kRowWarps * 32, kRowCtas) tree_rows16_kernel(const TreeParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
-    using Cache = typename std::conditional<kFp8, Tiles8<T, D>, Tiles16<T, D>>::type;
-    using Draft = Tiles16<T, D>;
+    using Cache = typename std::conditional<kFp8, Tiles8<T, D, kRows8>, Tiles16<T, D, kRows8>>::type;
+    using Draft = Tiles16<T, D, kRows8>;
     constexpr int kRing = kRowStages * (Cache::kBytes > Draft::kBytes ? Cache::kBytes : Draft::kBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - r * p.row_tiles) * 16;
@@ -645,25 +669,29 @@ struct TreeKernel {
     int smem;
 };
 
-template <typename T, int D, bool kFp8, typename TOut>
+template <typename T, int D, bool kFp8, bool kRows8, typename TOut>
 TreeKernel rows16() {
-    constexpr int ring8 = kFp8 ? Tiles8<T, D>::kBytes : 0, ring16 = Tiles16<T, D>::kBytes;
+    constexpr int ring8 = kFp8 ? Tiles8<T, D, kRows8>::kBytes : 0, ring16 = Tiles16<T, D, kRows8>::kBytes;
     constexpr int ring = kRowWarps * kRowStages * (ring8 > ring16 ? ring8 : ring16);
     constexpr int states = kRowWarps * 16 * (D + 2) * 4;
-    return TreeKernel{tree_rows16_kernel<T, D, kFp8, TOut>, ring > states ? ring : states};
+    return TreeKernel{tree_rows16_kernel<T, D, kFp8, kRows8, TOut>, ring > states ? ring : states};
 }
-template <typename T, int D, bool kFp8>
+template <typename T, int D, bool kFp8, bool kRows8>
 TreeKernel pick_out(int out_dtype) {
     switch (out_dtype) {
-        case LSE_MERGE_F32: return rows16<T, D, kFp8, float>();
-        case LSE_MERGE_F16: return rows16<T, D, kFp8, __half>();
-        default: return rows16<T, D, kFp8, __nv_bfloat16>();
+        case LSE_MERGE_F32: return rows16<T, D, kFp8, kRows8, float>();
+        case LSE_MERGE_F16: return rows16<T, D, kFp8, kRows8, __half>();
+        default: return rows16<T, D, kFp8, kRows8, __nv_bfloat16>();
     }
 }
+template <typename T, int D>
+TreeKernel pick_rows(bool fp8, bool rows8, int out_dtype) {
+    if (rows8) return fp8 ? pick_out<T, D, true, true>(out_dtype) : pick_out<T, D, false, true>(out_dtype);
+    return fp8 ? pick_out<T, D, true, false>(out_dtype) : pick_out<T, D, false, false>(out_dtype);
+}
 template <typename T>
-TreeKernel pick_tree(int D, bool fp8, int out_dtype) {
-    if (D == 64) return fp8 ? pick_out<T, 64, true>(out_dtype) : pick_out<T, 64, false>(out_dtype);
-    return fp8 ? pick_out<T, 128, true>(out_dtype) : pick_out<T, 128, false>(out_dtype);
+TreeKernel pick_tree(int D, bool fp8, bool rows8, int out_dtype) {
+    return D == 64 ? pick_rows<T, 64>(fp8, rows8, out_dtype) : pick_rows<T, 128>(fp8, rows8, out_dtype);
 }
 
 std::mutex g_tree_mu;
@@ -756,8 +784,8 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
         if (e == cudaSuccess)
             e = launch_tree_wide(p, a.dtype, fp8, a.R, a.out_dtype, a.B, a.Hkv, a.D, kPdl != 0, stream);
     } else {
-        const TreeKernel k = a.dtype == LSE_MERGE_F16 ? pick_tree<__half>(a.D, fp8, a.out_dtype)
-                                                      : pick_tree<__nv_bfloat16>(a.D, fp8, a.out_dtype);
+        const TreeKernel k = a.dtype == LSE_MERGE_F16 ? pick_tree<__half>(a.D, fp8, pl.rows <= 8, a.out_dtype)
+                                                      : pick_tree<__nv_bfloat16>(a.D, fp8, pl.rows <= 8, a.out_dtype);
         e = allow_smem((const void*)k.fn, k.smem);
         if (e == cudaSuccess) {
             cfg.gridDim = dim3((unsigned)(p.row_tiles * p.shards), (unsigned)a.Hkv, (unsigned)a.B);

@@ -526,41 +526,42 @@ __device__ __forceinline__ void issue(const WidePlan& pl, int s, uint32_t smem_u
 
 // ------------------------------------------------------------ queries
 
-// Query row -> row `row` of the tile at `tile` (or nowhere); e4m3: scaled to at
-// most 2^15 in f16, the inverse times `scale`.  A negative scale changes q's sign.
+// The warp's 32 query rows (lane's own at `src`, NULL: zeros) -> rows row0 .. row0 + 31
+// of the tile (or nowhere); e4m3: scaled to at most 2^15 in f16, the inverse times the
+// lane's `scale`.  A negative scale changes q's sign.  D / 8 lanes bring a row, all
+// rows' loads are in flight at once.
 template <typename T, int D, bool kFp8>
-__device__ __forceinline__ void load_query(const char* src, unsigned char* tile, int row, bool flip, float& scale) {
-    constexpr int CPR = D / 8;
+__device__ __forceinline__ void load_queries(const char* src, unsigned char* tile, int row0, int lane, bool flip,
+                                             float& scale) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, N = 32 / kRows;
     const uint32_t sign = flip ? 0x80008000u : 0u;
-    float up = 1.f;
-    if constexpr (kFp8) {
-        float big = 0.f;
-        if (src) {
-#pragma unroll 4
-            for (int c = 0; c < CPR; ++c) {
-                float f[8];
-                Elem<T>::unpack(*reinterpret_cast<const uint4*>(src + c * 16), f);
+    const int sub = lane / kLanes, ch = lane % kLanes;
+    uint4 u[N];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
-            }
-        }
-        const float top = fminf(fmaxf(pow2_below(big), 7.888609e-31f), 8.507059e37f);
-        up = 16384.f * pow2_inverse(top);
-        scale *= top * (1.f / 16384.f);
+    for (int i = 0; i < N; ++i) {
+        const uint64_t at = __shfl_sync(kFull, (uint64_t)src, i * kRows + sub);
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (at) u[i] = *reinterpret_cast<const uint4*>(at + ch * 16);
     }
-    if (!tile) return;
-#pragma unroll 4
-    for (int c = 0; c < CPR; ++c) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (src) u = *reinterpret_cast<const uint4*>(src + c * 16);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
         if constexpr (kFp8) {
-            float f[8];
-            Elem<T>::unpack(u, f);
-            u = make_uint4(Mma<__half>::pack(f[0] * up, f[1] * up), Mma<__half>::pack(f[2] * up, f[3] * up),
-                           Mma<__half>::pack(f[4] * up, f[5] * up), Mma<__half>::pack(f[6] * up, f[7] * up));
+            float f[8], big = 0.f;
+            Elem<T>::unpack(u[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+            const float top = fminf(fmaxf(pow2_below(big), 7.888609e-31f), 8.507059e37f);
+            const float up = 16384.f * pow2_inverse(top);
+            u[i] = make_uint4(Mma<__half>::pack(f[0] * up, f[1] * up), Mma<__half>::pack(f[2] * up, f[3] * up),
+                              Mma<__half>::pack(f[4] * up, f[5] * up), Mma<__half>::pack(f[6] * up, f[7] * up));
+            const float mine = __shfl_sync(kFull, top, lane % kRows * kLanes);
+            if (lane / kRows == i) scale *= mine * (1.f / 16384.f);
         }
-        *reinterpret_cast<uint4*>(tile + Lay<D>::at(row, c)) =
-            make_uint4(u.x ^ sign, u.y ^ sign, u.z ^ sign, u.w ^ sign);
+        if (tile)
+            *reinterpret_cast<uint4*>(tile + Lay<D>::at(row0 + i * kRows + sub, ch)) =
+                make_uint4(u[i].x ^ sign, u[i].y ^ sign, u[i].z ^ sign, u[i].w ^ sign);
     }
 }
 
@@ -810,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         float scale = fabsf(p.scale_log2);
         if (pl.n > 0) {
             const char* src = row < last_row ? q_row(p, x.b, x.hk, row) : nullptr;
-            load_query<T, D, kFp8>(src, pl.two || s == 0 ? smem + (pl.two ? s : 0) * L::kTile : nullptr, tid & 127,
-                                   p.scale_log2 < 0.f, scale);
+            load_queries<T, D, kFp8>(src, pl.two || s == 0 ? smem + (pl.two ? s : 0) * L::kTile : nullptr,
+                                     (warp & 3) * 32, lane, p.scale_log2 < 0.f, scale);
             if ((p.fold || x.drafts) && src) word = (uint64_t)p.tree[x.b * p.tree_b + row / p.G];
         }
         fence_async();
