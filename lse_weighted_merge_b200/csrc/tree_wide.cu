@@ -528,40 +528,44 @@ __device__ __forceinline__ void issue(const WidePlan& pl, int s, uint32_t smem_u
 
 // The warp's 32 query rows (lane's own at `src`, NULL: zeros) -> rows row0 .. row0 + 31
 // of the tile (or nowhere); e4m3: scaled to at most 2^15 in f16, the inverse times the
-// lane's `scale`.  A negative scale changes q's sign.  D / 8 lanes bring a row, all
-// rows' loads are in flight at once.
+// lane's `scale`.  A negative scale changes q's sign.  D / 8 lanes bring a row.
 template <typename T, int D, bool kFp8>
 __device__ __forceinline__ void load_queries(const char* src, unsigned char* tile, int row0, int lane, bool flip,
                                              float& scale) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, N = 32 / kRows;
     const uint32_t sign = flip ? 0x80008000u : 0u;
     const int sub = lane / kLanes, ch = lane % kLanes;
-    uint4 u[N];
+    // 8 loads in flight: straight code that runs once per block costs more in
+    // instruction fetches than a second round trip
+#pragma unroll 1
+    for (int b = 0; b < N; b += 8) {
+        uint4 u[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint64_t at = __shfl_sync(kFull, (uint64_t)src, i * kRows + sub);
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (at) u[i] = *reinterpret_cast<const uint4*>(at + ch * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if constexpr (kFp8) {
-            float f[8], big = 0.f;
-            Elem<T>::unpack(u[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
-#pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-            const float top = fminf(fmaxf(pow2_below(big), 7.888609e-31f), 8.507059e37f);
-            const float up = 16384.f * pow2_inverse(top);
-            u[i] = make_uint4(Mma<__half>::pack(f[0] * up, f[1] * up), Mma<__half>::pack(f[2] * up, f[3] * up),
-                              Mma<__half>::pack(f[4] * up, f[5] * up), Mma<__half>::pack(f[6] * up, f[7] * up));
-            const float mine = __shfl_sync(kFull, top, lane % kRows * kLanes);
-            if (lane / kRows == i) scale *= mine * (1.f / 16384.f);
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t at = __shfl_sync(kFull, (uint64_t)src, (b + i) * kRows + sub);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (at) u[i] = *reinterpret_cast<const uint4*>(at + ch * 16);
         }
-        if (tile)
-            *reinterpret_cast<uint4*>(tile + Lay<D>::at(row0 + i * kRows + sub, ch)) =
-                make_uint4(u[i].x ^ sign, u[i].y ^ sign, u[i].z ^ sign, u[i].w ^ sign);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (kFp8) {
+                float f[8], big = 0.f;
+                Elem<T>::unpack(u[i], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+#pragma unroll
+                for (int o = kLanes / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+                const float top = fminf(fmaxf(pow2_below(big), 7.888609e-31f), 8.507059e37f);
+                const float up = 16384.f * pow2_inverse(top);
+                u[i] = make_uint4(Mma<__half>::pack(f[0] * up, f[1] * up), Mma<__half>::pack(f[2] * up, f[3] * up),
+                                  Mma<__half>::pack(f[4] * up, f[5] * up), Mma<__half>::pack(f[6] * up, f[7] * up));
+                const float mine = __shfl_sync(kFull, top, lane % kRows * kLanes);
+                if (lane / kRows == b + i) scale *= mine * (1.f / 16384.f);
+            }
+            if (tile)
+                *reinterpret_cast<uint4*>(tile + Lay<D>::at(row0 + (b + i) * kRows + sub, ch)) =
+                    make_uint4(u[i].x ^ sign, u[i].y ^ sign, u[i].z ^ sign, u[i].w ^ sign);
+        }
     }
 }
 
@@ -594,117 +598,116 @@ struct Scores {
     uint64_t see;
 };
 
-// The largest score that the row sees, scaled.
+// Replace the scores by the scaled ones, -inf where not seen.
 template <bool kFp8>
-__device__ __forceinline__ float softmax_top(const Scores& x) {
-    float top = -INFINITY;
+__device__ __forceinline__ void scale_scores(Scores& x) {
 #pragma unroll 1
     for (int c = 0; c < kHK; c += 32) {
         float f[32];
         tm_ld32(x.at + c, f);
         const uint32_t see = (uint32_t)(x.see >> c);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-            const float k = kFp8 && x.k4 ? x.scale * reinterpret_cast<const float*>(x.k4)[c + u] : x.scale;
-            top = fmaxf(top, see >> u & 1 ? f[u] * k : -INFINITY);
+        for (int u = 0; u < 32; u += 4) {
+            float k[4] = {x.scale, x.scale, x.scale, x.scale};
+            if (kFp8 && x.k4) {
+                const float4 s = x.k4[(c + u) / 4];
+                k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[u + e] = see >> (u + e) & 1 ? f[u + e] * k[e] : -INFINITY;
         }
+        tm_put32(x.at + c, f);
     }
-    return top;
+    tm_wait_st();
+    x.scale = 1.f;
 }
 
-// S of a half tile -> P over it, in one pass over registers.  A row's first weights
-// are relative to 0: the maximum is then looked up and the pass made again, as it
-// is where weights leave fp32's range.
+// The largest score, scaled.
+__device__ __forceinline__ float largest_score(const Scores& x) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kHK; c += 32) {
+        float f[32];
+        tm_ld32(x.at + c, f);
+#pragma unroll
+        for (int u = 0; u < 32; u += 4) top = fmaxf(fmaxf(top, fmaxf(f[u], f[u + 1])), fmaxf(f[u + 2], f[u + 3]));
+    }
+    return top == -INFINITY ? top : top * x.scale;
+}
+
+// Scores -> weights relative to ref, with their sum l and the largest sum of 4, top.
+__device__ __forceinline__ void weigh(float (&f)[64], float scale, float ref, float& l, float& top) {
+    const uint64_t scale2 = pack2f(scale, scale), ref2 = pack2f(-ref, -ref);
+    uint64_t sum[4] = {0, 0, 0, 0};
+    top = 0.f;
+    // in steps over 32, so that each step's latencies overlap
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+        for (int u = c; u < c + 32; u += 2) {
+            uint64_t a = ref2;
+            fma2(a, pack2f(f[u], f[u + 1]), scale2);
+            unpack2f(a, f[u], f[u + 1]);
+        }
+#pragma unroll
+        for (int u = c; u < c + 32; ++u) f[u] = ex2(f[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint64_t t = pack2f(f[c + 2 * u], f[c + 2 * u + 1]);
+#pragma unroll
+            for (int h = 8; h < 32; h += 8)
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(pack2f(f[c + h + 2 * u], f[c + h + 2 * u + 1])));
+            float t0, t1;
+            unpack2f(t, t0, t1);
+            top = fmaxf(top, fmaxf(t0, t1));
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[u]) : "l"(t));
+        }
+    }
+    float s[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) unpack2f(sum[u], s[2 * u], s[2 * u + 1]);
+    l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+// S of a half tile -> P over it: one pass, made again with a higher reference in the
+// few halves where weights leave their range.  `ready`: all rows of the warp have a
+// reference.  The rare steps are short loops over TMEM, so that the instructions of
+// all halves stay near.
 template <typename TM, int D, bool kFp8>
-__device__ __forceinline__ void softmax_half(const Scores& x, uint32_t tO, float vref, uint32_t o_done, int seq,
-                                             volatile int* dead, RowSum& st) {
+__device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, float vref, uint32_t o_done, int seq,
+                                             volatile int* dead, bool& ready, RowSum& st) {
     using Bd = Bounds<TM>;
-    float f[64];
+    float f[64], l, top, down = 1.f;
     float (&fa)[32] = *reinterpret_cast<float (*)[32]>(f), (&fb)[32] = *reinterpret_cast<float (*)[32]>(f + 32);
-    float down = 1.f, l, top;
-    bool sought = false;
-    for (;;) {
+    if (x.each) scale_scores<kFp8>(x);
+    if (!ready) {
+        const float mx = largest_score(x);
+        if (st.m == -INFINITY && mx != -INFINITY) st.m = mx - Bd::kLow;   // (its sums are 0 so far)
+        ready = !__any_sync(kFull, st.m == -INFINITY);
+    }
+    for (int tries = 0;; ++tries) {
         tm_get32(x.at, fa);
         tm_get32(x.at + 32, fb);
-        const float ref = st.m == -INFINITY ? 0.f : st.m;
         tm_wait32(fa);
         tm_wait32(fb);
-        float scale = x.scale;
-        if (x.each) {
-#pragma unroll
-            for (int u = 0; u < 64; u += 4) {
-                float k[4] = {scale, scale, scale, scale};
-                if (kFp8 && x.k4) {
-                    const float4 s = x.k4[u / 4];
-                    k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    f[u + e] = (uint32_t)(x.see >> (u & 32)) >> (u + e & 31) & 1 ? f[u + e] * k[e] : -INFINITY;
-            }
-            scale = 1.f;
+        const float ref = st.m == -INFINITY ? 0.f : st.m;
+        weigh(f, x.scale, ref, l, top);
+        if (!__any_sync(kFull, top > Bd::kHigh) || tries == 2) break;
+        float next = ref;
+        if (top > Bd::kHigh)   // (past 2^24 the reference has steps above 1: by one at least)
+            next += fmaxf((float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase), fabsf(ref) * 1.8e-7f);
+        if (__any_sync(kFull, top == INFINITY)) {
+            const float mx = largest_score(x);
+            if (top == INFINITY) next = mx - Bd::kLow;
         }
-        const uint64_t scale2 = pack2f(scale, scale), ref2 = pack2f(-ref, -ref);
-        uint64_t sum[4] = {0, 0, 0, 0};
-        top = 0.f;
-        // in steps over 32, so that each step's latencies overlap
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-#pragma unroll
-            for (int u = c; u < c + 32; u += 2) {
-                uint64_t a = ref2;
-                fma2(a, pack2f(f[u], f[u + 1]), scale2);
-                unpack2f(a, f[u], f[u + 1]);
-            }
-#pragma unroll
-            for (int u = c; u < c + 32; ++u) f[u] = ex2(f[u]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint64_t t = pack2f(f[c + 2 * u], f[c + 2 * u + 1]);
-#pragma unroll
-                for (int h = 8; h < 32; h += 8)
-                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(pack2f(f[c + h + 2 * u], f[c + h + 2 * u + 1])));
-                float t0, t1;
-                unpack2f(t, t0, t1);
-                top = fmaxf(top, fmaxf(t0, t1));
-                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[u]) : "l"(t));
-            }
-        }
-        float s[8];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) unpack2f(sum[u], s[2 * u], s[2 * u + 1]);
-        l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-        if (!__any_sync(kFull, top > Bd::kHigh || st.m == -INFINITY)) break;
-        const bool seek = (top == INFINITY || st.m == -INFINITY) && !sought;
-        if (!__any_sync(kFull, seek)) {
-            float back = 1.f;
-            if (top > Bd::kHigh && top != INFINITY) {
-                // (past 2^24 the reference has steps above 1: by one at least)
-                const float rise = (float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase);
-                const float next = ref + fmaxf(rise, fabsf(ref) * 1.8e-7f);
-                back = ex2(ref - next);
-                st.m = next;
-            }
-#pragma unroll
-            for (int u = 0; u < 64; ++u) f[u] *= back;
-            l *= back;
-            down *= back;
-            break;
-        }
-        float mx = softmax_top<kFp8>(x);
-        if (seek && mx != -INFINITY) {
-            const float next = mx - Bd::kLow;
-            down = ex2(st.m - next);   // 0 at first
+        if (next != ref) {
+            const float a = ex2(ref - next);
+            down *= a;
+            st.l *= a;
             st.m = next;
         }
-        sought = true;
     }
-    st.l = st.l * down + l;
     if constexpr (kFp8) {
-        if (vref != st.vref) {
-            down *= st.vref * pow2_inverse(vref);
-            st.vref = vref;
-        }
         if (x.v4) {
 #pragma unroll
             for (int u = 0; u < 64; u += 4) {
@@ -716,19 +719,20 @@ __device__ __forceinline__ void softmax_half(const Scores& x, uint32_t tO, float
 #pragma unroll
     for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(Mma<TM>::pack(f[2 * u], f[2 * u + 1]));
     tm_put32(x.at, fa);
-    if (seq > 0 && __any_sync(kFull, down != 1.f)) {
+    st.l += l;
+    if (kFp8 && vref != st.vref) {
+        down *= st.vref * pow2_inverse(vref);
+        st.vref = vref;
+    }
+    if (__any_sync(kFull, down != 1.f) && seq > 0) {
         wait(o_done, (uint32_t)(seq - 1) & 1u, dead);   // P V of the half before is in
         tc_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-            tm_get32(tO + c, fa);
-            tm_get32(tO + c + 32, fb);
-            tm_wait32(fa);
-            tm_wait32(fb);
+        for (int c = 0; c < D; c += 32) {
+            tm_ld32(tO + c, fa);
 #pragma unroll
-            for (int u = 0; u < 64; ++u) f[u] *= down;
+            for (int u = 0; u < 32; ++u) fa[u] *= down;
             tm_put32(tO + c, fa);
-            tm_put32(tO + c + 32, fb);
         }
     }
     tm_wait_st();
@@ -820,43 +824,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         if (lane == 0) arrive(bars + 8 * kQFull);
         const bool idle = row - lane >= last_row;   // no live row in the warp
         const uint32_t tS = tmem + lanes + s * kTK, tO = tmem + lanes + 2 * kTK + s * D;
-        int seq = 0;
-        for (int i = 0; i < pl.count(s); ++i) {
-            const int j = pl.tile(s, i), keys = pl.keys(j), kslot = j % 3;
+        const int count = pl.count(s), step = pl.two ? 1 : 2;
+        const uint32_t s_full = bars + 8 * (kSFull + 2 * s), p_full = bars + 8 * (kPFull + 2 * s);
+        int seq = 0, kslot = pl.two ? 0 : s;
+        bool ready = false;   // all rows of the warp have a reference
+        for (int i = 0; i < count; ++i) {
+            const int j = pl.tile(s, i), keys = pl.keys(j);
+            float tile_scale = scale, vref = 1.f;
+            float4 info = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int half = 0; half < 2 && half * kHK < keys; ++half, ++seq) {
-                const int left = keys - half * kHK, buf = seq & 1;
-                Scores sc{tS + buf * kHK, scale, left < kHK || j >= pl.cached, nullptr, nullptr, 0.f, ~0ull};
-                if (sc.each) {
-                    if (left < kHK) sc.see = (1ull << left) - 1;
-                    if (j >= pl.cached) sc.see &= word;
-                }
-                wait(bars + 8 * (kSFull + 2 * s + buf), (uint32_t)(seq >> 1) & 1u, &ctrl->dead);
+            for (int half = 0; half * kHK < keys; ++half, ++seq) {
+                const int buf = seq & 1;
+                wait(s_full + 8 * buf, (uint32_t)(seq >> 1) & 1u, &ctrl->dead);
                 tc_after();
                 if (!idle) {
-                    float vref = 1.f;
-                    if constexpr (kFp8) {
-                        const float4 t = ctrl->tile[kslot];
-                        vref = t.y;
-                        sc.scale *= t.x;
-                        if (t.x == 0.f) {
-                            sc.scale = scale;
-                            sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK + half * kHK);
-                            sc.each = true;
-                        }
-                        if (t.z != 0.f) {
-                            wait(bars + 8 * (kVFull + j % 2), (uint32_t)(j / 2) & 1u, &ctrl->dead);   // their scales
-                            sc.v4 = reinterpret_cast<const float4*>(vs + j % 2 * kTK + half * kHK);
-                            sc.vinv = pow2_inverse(vref);
-                            __syncwarp();
-                        }
+                    if (kFp8 && half == 0) {
+                        info = ctrl->tile[kslot];
+                        vref = info.y;
+                        tile_scale = scale * info.x;
                     }
-                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + s), seq, &ctrl->dead, st);
+                    const int left = keys - half * kHK;
+                    Scores sc{tS + buf * kHK, tile_scale, left < kHK || j >= pl.cached, nullptr, nullptr, 0.f, ~0ull};
+                    if (sc.each) {
+                        if (left < kHK) sc.see = (1ull << left) - 1;
+                        if (j >= pl.cached) sc.see &= word;
+                    }
+                    if (kFp8 && info.x == 0.f) {
+                        sc.scale = scale;
+                        sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK + half * kHK);
+                        sc.each = true;
+                    }
+                    if (kFp8 && info.z != 0.f) {
+                        wait(bars + 8 * (kVFull + j % 2), (uint32_t)(j / 2) & 1u, &ctrl->dead);   // their scales
+                        sc.v4 = reinterpret_cast<const float4*>(vs + j % 2 * kTK + half * kHK);
+                        sc.vinv = pow2_inverse(vref);
+                        __syncwarp();
+                    }
+                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + s), seq, &ctrl->dead, ready, st);
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive(bars + 8 * (kPFull + 2 * s + buf));
+                if (lane == 0) arrive(p_full + 8 * buf);
             }
+            kslot += step;
+            if (kslot >= 3) kslot -= 3;
         }
         const int last = seq - 1;   // the last P V
         if (last >= 0) wait(bars + 8 * (kODone + s), (uint32_t)last & 1u, &ctrl->dead);
