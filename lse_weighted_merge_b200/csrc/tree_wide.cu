@@ -755,7 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait();
+    // The launch before a joining one is that of the drafts, and its blocks wait for
+    // what precedes it before they let this one start: only their partials are still
+    // to come, and are waited for at the end.
+    if (!p.join) pdl_wait();
     pdl_release();
 
     const int block = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - block * p.row_tiles) * 256, rows = p.T * p.G;
@@ -897,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     }
     soft_sync();
     const bool dead = ctrl->dead != 0;
+    if (p.join) pdl_wait();
     {
         // with one row tile, stream 1 has the second one's rows here: all dead
         const int row = row0 + 128 * s + (tid & 127);
