@@ -346,9 +346,10 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         int64_t step;
         int key;
     };
-    auto fetch = [&](Source& f, uint32_t dst) {
+    // (nothing past the end is fetched: the merge of the streams reuses the space)
+    auto fetch = [&](Source& f, uint32_t dst, bool more) {
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
+        for (int u = 0; more && u < N; ++u) {
             const bool ok = f.key < x.hi;
             cp_async16(smem_u + dst + u * kLoadWarps * 512 + lane * 16, ok ? f.at : f.base, ok ? 16 : 0);
             f.at += f.step;
@@ -424,8 +425,8 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
     Source k{x.kb + col, x.kb + (x.lo + row0) * p.k_l + col, kStep * p.k_l, x.lo + row0};
     Source v{x.vb + col, x.vb + (x.lo + row0) * p.v_l + col, kStep * p.v_l, x.lo + row0};
     for (int j = 0; j < ahead; ++j) {
-        fetch(k, raw(0, j));
-        fetch(v, raw(1, j));
+        fetch(k, raw(0, j), j < pl.n);
+        fetch(v, raw(1, j), j < pl.n);
     }
     Ring kr{2, 0, 1}, vr{2, 0, 1};
     float run = 1.17549435e-38f;   // the reference of the values' scales
@@ -460,7 +461,7 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         kr.next();
         if (++kslot == 3) kslot = 0;
         sk.next(x.hi);
-        fetch(k, raw(0, j));
+        fetch(k, raw(0, j), j + ahead < pl.n);
         landed();
         wait(bars + 8 * (kVEmpty + vr.slot), vr.phase, &ctrl->dead);
         convert(smem + (4 + vr.slot) * L::kTile, raw(1, j), vplain, sv, pow2_inverse(run));
@@ -469,7 +470,7 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         if (lane == 0) arrive(bars + 8 * (kVFull + vr.slot));
         vr.next();
         sv.next(x.hi);
-        fetch(v, raw(1, j));
+        fetch(v, raw(1, j), j + ahead < pl.n);
     }
     cp_wait<0>();
 }
