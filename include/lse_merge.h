@@ -340,7 +340,9 @@ int lse_merge_kv_dequantize(const lse_merge_kv_args* args, lse_merge_stream_t st
  *                at the same time need workspaces of their own
  *   q, k, v, the drafts and out_o are 16-byte aligned, with strides of whole 16-byte
  *   multiples; scale strides are any >= 0; a tree word is 8-byte aligned
- * One launch, or two where partials are merged.  Returns the codes of
+ * One launch, and one more each where partials are merged and where drafts of
+ * more than 16 query rows per KV head (T * Hq / Hkv) meet an e4m3 cache.  Scales that
+ * are powers of two, as quantize writes them, are fastest.  Returns the codes of
  * lse_merge; LSE_MERGE_EUNSUP for a D, T, group size or dtype outside the above.
  */
 #define LSE_MERGE_TREE_MAX_T 64

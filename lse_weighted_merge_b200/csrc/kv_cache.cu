@@ -11,9 +11,13 @@
 // 448 either way), not precision.  e is read off the bits of a: 448 = 1.75 * 2^8,
 // so e = exponent(a) - 8, and one more where the mantissa is above 1.75.
 //
-// Both kernels are bound by memory.  D / 8 lanes hold a row, 8 elements each
-// (16 bytes of a 16-bit type, 8 bytes of codes); the row maximum is a shuffle
-// over those lanes.
+// Both kernels are bound by memory.  Writing 16 x 4096 tokens of 8 heads, D = 128,
+// bf16, takes 66 to 71 us by box (5.8 to 6.1 TB/s, 88 to 92 % of the measured copy rate).  With
+// the tests for infinities on every element it was bound by the compares (98 us):
+// the maximum is taken over the magnitudes' bits, two 16-bit ones per instruction,
+// and shows infinities and NaN by itself.  Four rows per group of lanes took 168 us
+// (registers).  Reading them back: 70 to 75 us, 83 to 88 %, two rows per group of lanes;
+// the loads kept out of L1 (81 us without).  Few rows are bound by the launch: 3.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

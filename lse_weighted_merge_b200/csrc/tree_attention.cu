@@ -3,9 +3,10 @@
 // tokens' own keys, which a mask selects (a tree of drafted tokens).
 //
 // The work is cut as the merge likes it: the cached keys of a (sequence, KV
-// head) into R shards, and the drafts' keys as one more shard, the only one
-// with a mask.  Every shard gives (o, lse) partials in fp32 and the LSE merge
-// combines them; a lone shard writes the result itself.
+// head) into R shards.  The drafts' keys are one more shard (rows16 kernel, or an
+// e4m3 cache) or a tile of the last one (tree_wide.cu).  Every shard gives (o, lse)
+// partials in fp32 and the LSE merge combines them; a lone shard writes the result
+// itself.
 //
 // The query rows of a (sequence, KV head) are the T * G pairs (token, head of
 // the group), row = t * G + g: all of them read the same keys.
@@ -26,8 +27,14 @@
 //     multiplies its score.  A value's scale w multiplies its weight p before
 //     the rounding to f16, relative to a power of two near the largest scale
 //     that the warp has seen.
-//   * With f16 weights p the softmax reference lies 2^10 below the running
-//     maximum: weights down to 2^-24 of the largest keep f16's 11 bits.
+//   * Up to 8 rows (a decode step, mostly) leave the products' rows 8 to 15 empty;
+//     nothing but the products is then done for them.
+// Measured on B200, 64 sequences of 4096 e4m3 tokens, 32 heads over 8, D = 128:
+// 97 to 107 us by box, 5.2 to 5.7 TB/s, 79 to 88 % of the measured copy rate.  Bound by the
+// instructions per key (codes to f16, products that use 4 of 16 rows): 53 % of the
+// issue slots with two warps per scheduler.  Three CTAs per SM with two stages each
+// took 112 us (512 CTAs leave a tail), scaling o in every tile and all rows' softmax
+// 119.  One sequence, 16 shards: 9.7 us with the merge, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

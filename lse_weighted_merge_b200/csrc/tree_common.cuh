@@ -57,7 +57,7 @@ __device__ __forceinline__ Shard shard_of(const TreeParams& p, int r, int hk, in
     x.b = b;
     x.hk = hk;
     x.r = r;
-    x.live = p.draft_len ? min(max(p.draft_len[b], 0), p.T) : p.T;
+    x.live = p.draft_len ? min(max(__ldcg(p.draft_len + b), 0), p.T) : p.T;
     x.drafts = r == p.R;
     if (x.drafts) {
         x.lo = 0;
@@ -65,7 +65,7 @@ __device__ __forceinline__ Shard shard_of(const TreeParams& p, int r, int hk, in
         x.kb = p.kd + b * p.kd_b + hk * p.kd_h;
         x.vb = p.vd + b * p.vd_b + hk * p.vd_h;
     } else {
-        const int len = p.kv_len ? min(max(p.kv_len[b], 0), p.L) : p.L;
+        const int len = p.kv_len ? min(max(__ldcg(p.kv_len + b), 0), p.L) : p.L;
         const int per = (int)(((int64_t)len + p.R - 1) / p.R);
         x.lo = (int)min((int64_t)len, (int64_t)r * per);
         x.hi = (int)min((int64_t)len, (int64_t)x.lo + per);

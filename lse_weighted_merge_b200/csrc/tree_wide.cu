@@ -9,28 +9,36 @@
 //   * up to 128 rows: both streams have the same rows, stream s the key tiles
 //     s, s + 2, ...; their states are merged at the end, in shared memory.
 // Warps 0-3 and 4-7 are the softmax of stream 0 and 1 (thread = query row = TMEM
-// lane; one thread of each also issues the stream's products), warps 8-15 bring
-// the tiles:
-//   S = Q K^T   128 x 128, Q and K in shared memory (K-major, 128-byte swizzle)
+// lane), warps 8-15 bring the tiles, one thread of warps 16 and 17 each issues the
+// products of a stream, in halves of a tile:
+//   S = Q K^T   128 x 64, Q and K in shared memory (K-major, 128-byte swizzle)
 //   O += P V    128 x D, P in TMEM over S (16 bits, half its columns), V in shared
 //               memory as it lies in the cache (its D is the fast index: MN-major)
-// TMEM: S0 | S1 | O0 | O1.  The order "QK of tile i + 1 after PV of tile i" of
-// each stream makes S complete imply O complete, so a softmax thread may scale
-// its row of O when it has seen S.  It does so only where the running maximum has
-// grown by 2^kHigh over the reference: the reference lies kLow .. kHigh below the
-// maximum, and what it is drops out at the end.
+// TMEM: S0 | S1 (two buffers of 64 columns each) | O0 | O1.  While a softmax warp is
+// in one half, the other buffer's S is made.  Weights are relative to a reference
+// that lies below the row's maximum and hardly ever moves; where it does, the
+// thread waits for the stream's last P V and scales its row of O.
 //
-// 16-bit tiles come by cp.async into the swizzled layout.  e4m3 tiles come by
-// cp.async as they are, each thread converts the 16-byte chunks that it fetched
-// itself to f16 (exact) and stores them swizzled; q is scaled per row by a power
-// of two, a key's scale multiplies its score and a value's scale its weight,
-// relative to a power of two near the largest scale so far (as in the rows16
-// kernel).  Keys past the shard's end are zeros, so that no value there, whatever
-// it is, meets a weight of 0.
+// 16-bit tiles come by cp.async into the swizzled layout; the drafts are a tile of
+// the last shard, the only one with a mask row by row.  e4m3 tiles come by cp.async
+// as they are; each warp converts what it fetched to f16 (exact) and stores it
+// swizzled.  q is scaled per row by a power of two.  Scales that are powers of two
+// (as lse_merge_kv_quantize writes them) go into the f16 tiles, exactly; others
+// multiply scores and weights one by one.  The drafts of an e4m3 cache, whose
+// products are of another type, are a launch of their own; a lone cached shard
+// joins their partial.  Keys past the shard's end are zeros, so that no value
+// there, whatever it is, meets a weight of 0.
 //
-// The exponentials (16 per clock and SM) and the tensor cores (128 x 128 x 256
-// multiply-adds per tile at 4096 per clock) bound it alike: 1024 clocks per tile
-// of 128 rows and 128 keys each.
+// Measured on B200, 16 trees of 64 drafts, 32 heads over 8, D = 128, 8192 e4m3
+// tokens: 224 us, 612 TFLOP/s (the rows16 kernel: 913); 16 trees of 16 over 4096
+// bf16 tokens: 58 to 66 us, 4.2 to 4.6 TB/s (186).  The exponentials (16 per clock and SM)
+// and the tensor cores bound a tile of 128 rows and 128 keys at 1024 clocks alike;
+// a softmax warp takes about 2500 clocks for a half, of which the exponentials are
+// 512: its own chain of barrier, TMEM load, weights, TMEM store and barrier, not a
+// unit, is what is left (no unit is busy more than 30 % of the time).  Taking the
+// exponentials out saves 19 %, the products 7 %, the conversion 5 %.  Two threads
+// per row (16 softmax warps) gave 236 us, halves of 128 keys with one buffer 207
+// instead of 199 for the cached part, a prefetch into L2 four tiles ahead nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,7 +59,7 @@ constexpr int kLoadWarps = 8;
 constexpr int kThreads = (8 + kLoadWarps + 4) * 32;
 // Registers per thread of the softmax, loading and issuing warps: together at most
 // what the block is launched with.
-constexpr int kSoftRegs = 136, kLoadRegs = 80, kIssueRegs = 40, kLaunchRegs = 96;
+constexpr int kSoftRegs = 144, kLoadRegs = 72, kIssueRegs = 40, kLaunchRegs = 96;
 static_assert(256 * kSoftRegs + kLoadWarps * 32 * kLoadRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs &&
               kThreads * kLaunchRegs <= 65536 && kThreads * (kLaunchRegs + 8) > 65536, "registers");
 constexpr int kTK = 128;                    // keys per tile
@@ -301,7 +309,7 @@ __device__ __forceinline__ void load16(const TreeParams& p, const Shard& x, cons
             bool bad = false;
             for (int row = row0; row < kTK; row += kRows) {
                 uint4 u = make_uint4(0, 0, 0, 0);
-                if (row < t.count) u = *reinterpret_cast<const uint4*>(src + row * stride);
+                if (row < t.count) u = __ldcg(reinterpret_cast<const uint4*>(src + row * stride));
                 uint32_t c[4] = {u.x, u.y, u.z, u.w};
                 bad |= scrub16<T>(c);
                 *reinterpret_cast<uint4*>(smem + slot * L::kTile + L::at(row, ch)) = make_uint4(c[0], c[1], c[2], c[3]);
@@ -368,10 +376,10 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
             const float* at = src;
             if (key + 96 < hi) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = *at;
+                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = __ldcg(at);
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = key + 32 * e < hi ? *at : 0.f;
+                for (int e = 0; e < 4; ++e, at += 32 * stride) v[e] = key + 32 * e < hi ? __ldcg(at) : 0.f;
             }
             src = at;
             key += kTK;
@@ -545,7 +553,7 @@ __device__ __forceinline__ void load_queries(const char* src, unsigned char* til
         for (int i = 0; i < 8; ++i) {
             const uint64_t at = __shfl_sync(kFull, (uint64_t)src, (b + i) * kRows + sub);
             u[i] = make_uint4(0, 0, 0, 0);
-            if (at) u[i] = *reinterpret_cast<const uint4*>(at + ch * 16);
+            if (at) u[i] = __ldcg(reinterpret_cast<const uint4*>(at + ch * 16));
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -693,7 +701,15 @@ __device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, float vref, 
         tm_wait32(fb);
         const float ref = st.m == -INFINITY ? 0.f : st.m;
         weigh(f, x.scale, ref, l, top);
-        if (!__any_sync(kFull, top > Bd::kHigh) || tries == 2) break;
+        // where scores are so large that a fused difference could lie far from that of
+        // the rounded scores, which the reference is made from, they are rounded first
+        const bool large = !x.each && fabsf(ref) > 4194304.f;
+        if (!__any_sync(kFull, top > Bd::kHigh || large) || tries == 3) break;
+        if (__any_sync(kFull, large)) {
+            scale_scores<kFp8>(x);
+            x.each = true;
+            continue;
+        }
         float next = ref;
         if (top > Bd::kHigh)   // (past 2^24 the reference has steps above 1: by one at least)
             next += fmaxf((float)((int)(__float_as_uint(top) >> 23) - 127 - Bd::kBase), fabsf(ref) * 1.8e-7f);
@@ -821,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             const char* src = row < last_row ? q_row(p, x.b, x.hk, row) : nullptr;
             load_queries<T, D, kFp8>(src, pl.two || s == 0 ? smem + (pl.two ? s : 0) * L::kTile : nullptr,
                                      (warp & 3) * 32, lane, p.scale_log2 < 0.f, scale);
-            if ((p.fold || x.drafts) && src) word = (uint64_t)p.tree[x.b * p.tree_b + row / p.G];
+            if ((p.fold || x.drafts) && src) word = (uint64_t)__ldcg(p.tree + x.b * p.tree_b + row / p.G);
         }
         fence_async();
         __syncwarp();

@@ -113,3 +113,82 @@ def test_repeats_are_the_same_bits():
         for _ in range(20):
             out, lse = c.run()
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("kind", KINDS)
+def test_scores_past_fp32s_integers(kind, T):
+    """Scores so large that fp32 has steps of hundreds between them: one key takes all
+    the weight, or several share it; rows stay finite and inside their values."""
+    c = Case(kind, 2, T, 8, 2, 300, 64)
+    for scale in (1e7, -3e8):
+        out, lse = c.run(scale=scale, out_dtype=torch.float32)
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+        top = max(float(c.whole("v").abs().max()), float(c.vd.double().abs().max()))
+        assert float(out.abs().max()) <= top * (1 + 2.0 ** -7)
+
+
+@pytest.mark.parametrize("kind", ["bf16+e4m3", "f16+e4m3"])
+@pytest.mark.parametrize("T", [3, 24, 64])
+def test_scales_that_are_no_powers_of_two(kind, T):
+    """Any positive scales, some tiles with, some without powers of two, some whose
+    scales lie further apart than f16 reaches."""
+    c = Case(kind, 2, T, 8, 2, 900, 128)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for name in ("k_scale", "v_scale"):
+        s = c.scales[name]
+        s[:, :, 128:256] *= 1 + torch.rand(2, 2, 128, generator=g, device="cuda")
+        s[:, :, 300:310] *= 2.0 ** -20
+        s[:, 1, 500:640] *= 1.25
+    c.scales["v_scale"][0, :, 700:] *= 2.0 ** 9
+    for splits in (1, 3, None):
+        c.check(splits=splits, out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("kind", ["bf16+e4m3", "bf16"])
+def test_one_shard_with_drafts_in_graphs(kind):
+    """The lone cached shard that joins the drafts' partial, captured behind the
+    writes of its inputs, replayed on two streams at once."""
+    cases = [Case(kind, 2, 48, 8, 2, 500, 128, seed=i) for i in (1, 2)]
+    eager = [c.run(splits=1) for c in cases]
+    torch.cuda.synchronize()
+    graphs, outs, held = [], [], [c.q.clone() for c in cases]
+    for c, q in zip(cases, held):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.q.copy_(q)
+            outs.append(c.run(splits=1))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for c in cases:
+        c.q.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (o, l), (eo, el) in zip(outs, eager):
+        assert torch.equal(o, eo) and torch.equal(l, el)
+
+
+def test_written_then_attended_without_a_pause():
+    """A prompt written and attended over in one stream, again and again with other
+    contents: every call sees the writes before it."""
+    B, T, Hq, Hkv, L, D = 4, 32, 16, 2, 400, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    c = Case("bf16+e4m3", B, T, Hq, Hkv, L, D)
+    ks, vs = c.scales["k_scale"], c.scales["v_scale"]
+    start = ints([0] * B)
+    prompts = [[torch.randn(B, Hkv, L, D, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv"] for _ in range(6)]
+    got, wholes = [], []
+    for k, v in prompts:
+        lm.kv_quantize_(c.k, c.v, ks, vs, k, v, start)
+        got.append(c.run(splits=1))
+        got.append(c.run(splits=3))
+        wholes.append([c.whole("k"), c.whole("v")])
+    torch.cuda.synchronize()
+    for i, (k, v) in enumerate(wholes):
+        ref = attention(c.q, k, v, c.kd, c.vd, c.tree)
+        for o, l in got[2 * i:2 * i + 2]:
+            check(o, l, ref, c.wt)
