@@ -16,12 +16,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblse_merge.so")
-SOURCES = [os.path.join(CSRC, "plan.cpp"), os.path.join(CSRC, "lse_merge.cu"),
+SOURCES = [os.path.join(CSRC, "plan.cpp"), os.path.join(CSRC, "kv_plan.cpp"), os.path.join(CSRC, "lse_merge.cu"),
            os.path.join(CSRC, "decode_attention.cu"), os.path.join(CSRC, "cp_exchange.cu"),
            os.path.join(CSRC, "kv_cache.cu"), os.path.join(CSRC, "tree_attention.cu"),
            os.path.join(CSRC, "tree_wide.cu"),
            os.path.join(CSRC, "host_pipeline.cpp")]
-HEADERS = [os.path.join(INCLUDE, "lse_merge.h"), os.path.join(CSRC, "plan.h"),
+HEADERS = [os.path.join(INCLUDE, "lse_merge.h"), os.path.join(CSRC, "plan.h"), os.path.join(CSRC, "kv_plan.h"),
            os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_common.cuh"),
            os.path.join(CSRC, "tree_common.cuh")]
 

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "device_common.cuh"
+#include "kv_plan.h"
 #include "lse_merge.h"
 #include "plan.h"
 

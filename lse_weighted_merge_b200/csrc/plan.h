@@ -163,21 +163,6 @@ int make_attn_plan(const void* q, const void* k, const void* v, int B, int Hq, i
 int attn_workspace_layout(int B, int Hq, int Hkv, int R, int D, AttnPlan* plan);
 lse_merge_attn_strides default_attn_strides(int Hq, int Hkv, int L, int D);
 
-// 8-bit cache, write and read back: check the arguments (`write`: quantize).
-int check_kv_args(const lse_merge_kv_args& a, bool write);
-
-// Attention over a cache and drafts: validated geometry.
-struct TreePlan {
-    int G;             // query heads per KV head
-    int rows;          // query rows of one (sequence, KV head): T * G
-    int shards;        // R, and one more for the drafts
-    int64_t ws_l_off;  // workspace: partial o [B, T, Hq, shards, D] fp32, then lse [B, T, Hq, shards]
-    int64_t ws_bytes;  // 0 when one shard writes the result itself
-};
-int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* plan);
-int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan);
-int tree_default_splits(int B, int T, int Hq, int Hkv, int L, int D, int sms);
-
 // Validate the arguments of lse_merge_state_update and fill *plan.
 int make_state_plan(const void* o_acc, const float* lse_acc, const void* o_new,
                     const float* lse_new, int B, int H, int D, const lse_merge_state_strides& st,

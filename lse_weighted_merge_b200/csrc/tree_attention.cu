@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "kv_plan.h"
 #include "lse_merge.h"
 #include "plan.h"
 #include "tree_common.cuh"
