@@ -11,13 +11,14 @@
 // 448 either way), not precision.  e is read off the bits of a: 448 = 1.75 * 2^8,
 // so e = exponent(a) - 8, and one more where the mantissa is above 1.75.
 //
-// Both kernels are bound by memory.  Writing 16 x 4096 tokens of 8 heads, D = 128,
-// bf16, takes 66 to 71 us by box (5.8 to 6.1 TB/s, 88 to 92 % of the measured copy rate).  With
-// the tests for infinities on every element it was bound by the compares (98 us):
-// the maximum is taken over the magnitudes' bits, two 16-bit ones per instruction,
-// and shows infinities and NaN by itself.  Four rows per group of lanes took 168 us
-// (registers).  Reading them back: 70 to 75 us, 83 to 88 %, two rows per group of lanes;
-// the loads kept out of L1 (81 us without).  Few rows are bound by the launch: 3.3 us.
+// Both kernels are bound by memory, with 16 elements of a row per lane.  Writing
+// 16 x 4096 tokens of 8 heads, D = 128, bf16, takes 66 to 71 us by box (5.8 to 6.1
+// TB/s, 88 to 92 % of the measured copy rate).  With tests for infinities on every
+// element it was bound by the compares (98 us): the maximum is taken over the
+// magnitudes' bits, two 16-bit ones per instruction, and shows infinities and NaN
+// by itself.  Four rows per group of lanes took 168 us (registers).  Reading them
+// back: 62 us, the measured copy rate (8 codes per lane: 71 to 75; loads that stay
+// in L1: 81).  Few rows are bound by the launch: 3.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -211,67 +212,59 @@ __global__ void __launch_bounds__(256) kv_quantize_kernel(const KvParams p) {
     }
 }
 
-template <typename T, int D, int U>
+// D / 16 lanes per row, the same two runs.
+template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_dequantize_kernel(const KvParams p) {
-    constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
+    constexpr int kLanes = D / 16, E = (int)sizeof(T);
     pdl_wait();
     pdl_release();
+    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
-    uint2 w[U][2];
-    float sc[U][2];
-    int64_t to[U][2];
-    bool in[U];
+    if (i >= p.rows) return;
+    int b, h, j;
+    row_of(p, i, b, h, j);
+    const int pos = (int)min((int64_t)p.start[b] + j, (int64_t)INT32_MAX);
+    const bool there = pos >= 0 && pos < p.L && (!p.count || j < p.count[b]);
+    uint2 w[2][2] = {};
+    float sc[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t i = (blockIdx.x * U + u) * kGroups + threadIdx.x / kLanes;
-        in[u] = i < p.rows;
-        int b, h, j;
-        row_of(p, min(i, p.rows - 1), b, h, j);
-        const int pos = (int)min((int64_t)p.start[b] + j, (int64_t)INT32_MAX);
-        const bool there = in[u] && pos >= 0 && pos < p.L && (!p.count || j < p.count[b]);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            w[u][s] = make_uint2(0u, 0u);
-            sc[u][s] = 0.f;
-            to[u][s] = b * p.x_b[s] + h * p.x_h[s] + j * p.x_t[s];
-            if (there) {
-                w[u][s] = ld8(p.cache[s] + b * p.c_b[s] + h * p.c_h[s] + pos * p.c_l[s] + lane * 8);
-                sc[u][s] = p.scale[s][b * p.s_b[s] + h * p.s_h[s] + pos * p.s_l[s]];
-            }
+    for (int s = 0; s < 2; ++s) {
+        if (there) {
+            const char* from = p.cache[s] + b * p.c_b[s] + h * p.c_h[s] + pos * p.c_l[s] + lane * 8;
+            w[s][0] = ld8(from);
+            w[s][1] = ld8(from + D / 2);
+            sc[s] = p.scale[s][b * p.s_b[s] + h * p.s_h[s] + pos * p.s_l[s]];
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (!in[u]) continue;
+    for (int s = 0; s < 2; ++s) {
+        char* to = p.x[s] + b * p.x_b[s] + h * p.x_h[s] + j * p.x_t[s] + lane * 8 * E;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int r = 0; r < 2; ++r) {
             float f[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 v = from_e4m3x2((k < 2 ? w[u][s].x : w[u][s].y) >> (16 * (k & 1)) & 0xffffu);
-                f[2 * k] = v.x * sc[u][s];
-                f[2 * k + 1] = v.y * sc[u][s];
+                const float2 v = from_e4m3x2((k < 2 ? w[s][r].x : w[s][r].y) >> (16 * (k & 1)) & 0xffffu);
+                f[2 * k] = v.x * sc[s];
+                f[2 * k + 1] = v.y * sc[s];
             }
-            store_vec<T, 8>(p.x[s] + to[u][s] + lane * 8 * (int)sizeof(T), f);
+            store_vec<T, 8>(to + r * (D / 2) * E, f);
         }
     }
 }
 
 using KvFn = void (*)(KvParams);
 
-constexpr int kManyRows = 2;   // rows read back per group of lanes where there are many
-
 template <typename T>
-KvFn pick_d(bool write, bool many, int D) {
+KvFn pick_d(bool write, int D) {
     if (write) return D == 64 ? kv_quantize_kernel<T, 64> : kv_quantize_kernel<T, 128>;
-    if (many) return D == 64 ? kv_dequantize_kernel<T, 64, kManyRows> : kv_dequantize_kernel<T, 128, kManyRows>;
-    return D == 64 ? kv_dequantize_kernel<T, 64, 1> : kv_dequantize_kernel<T, 128, 1>;
+    return D == 64 ? kv_dequantize_kernel<T, 64> : kv_dequantize_kernel<T, 128>;
 }
-KvFn pick(bool write, bool many, int dtype, int D) {
+KvFn pick(bool write, int dtype, int D) {
     switch (dtype) {
-        case LSE_MERGE_F32: return pick_d<float>(write, many, D);
-        case LSE_MERGE_F16: return pick_d<__half>(write, many, D);
-        default: return pick_d<__nv_bfloat16>(write, many, D);
+        case LSE_MERGE_F32: return pick_d<float>(write, D);
+        case LSE_MERGE_F16: return pick_d<__half>(write, D);
+        default: return pick_d<__nv_bfloat16>(write, D);
     }
 }
 
@@ -308,9 +301,7 @@ int launch(const lse_merge_kv_args* args, bool write, cudaStream_t stream) {
     p.div0 = fastdiv_c(p.n0);
     p.div1 = fastdiv_c(p.n1);
     p.rows = (uint32_t)a.B * p.n0 * p.n1;
-    // (many: one row each would still fill the GPU's 148 x 2048 threads twice over)
-    const bool many = !write && (int64_t)p.rows * (a.D / 8) > 2 * kManyRows * 148 * 2048;
-    const uint32_t per = write ? 256u / (uint32_t)(a.D / 16) : 256u / (uint32_t)(a.D / 8) * (many ? kManyRows : 1);
+    const uint32_t per = 256u / (uint32_t)(a.D / 16);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.rows + per - 1) / per);
     cfg.blockDim = dim3(256);
@@ -320,7 +311,7 @@ int launch(const lse_merge_kv_args* args, bool write, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPdl ? 1 : 0;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, pick(write, many, a.dtype, a.D), p);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, pick(write, a.dtype, a.D), p);
     if (err != cudaSuccess) {
         set_last_cuda_error((int)err);
         (void)cudaGetLastError();
