@@ -46,3 +46,7 @@ def test_default_splits():
                              (1, 1, 1, 1, 1), (2, 5, 8, 8, 63)):
         R = d(B, T, Hq, Hkv, L, 128, 148)
         assert 1 <= R <= 64 and (R == 1 or R <= -(-L // 32))
+
+
+def test_status_needs_a_place_for_its_answer():
+    assert nat.lib.lse_merge_tree_status(None) == nat.ENULL
