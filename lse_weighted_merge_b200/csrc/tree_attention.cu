@@ -30,9 +30,10 @@
 //   * Up to 8 rows (a decode step, mostly) leave the products' rows 8 to 15 empty;
 //     nothing but the products is then done for them.
 // Measured on B200, 64 sequences of 4096 e4m3 tokens, 32 heads over 8, D = 128:
-// 97 to 107 us by box, 5.2 to 5.7 TB/s, 79 to 88 % of the measured copy rate.  Bound by the
-// instructions per key (codes to f16, products that use 4 of 16 rows): 53 % of the
-// issue slots with two warps per scheduler.  Three CTAs per SM with two stages each
+// 103 us, 5.4 TB/s, 82 % of the measured copy rate (97 us where the keys of the call
+// before are partly in L2 still).  Bound by the instructions per key (codes to f16,
+// products that use 4 of 16 rows) and their latencies: two warps per scheduler use 42
+// to 53 % of the issue slots.  With tests in full tiles too: 106.  Three CTAs per SM with two stages each
 // took 112 us (512 CTAs leave a tail), scaling o in every tile and all rows' softmax
 // 119.  One sequence, 16 shards: 9.7 us with the merge, latency.
 #include <cuda_bf16.h>
@@ -283,14 +284,25 @@ struct Tiles8 {
     __device__ static void issue(const TreeParams& p, const Shard& x, int key0, uint32_t st, int lane) {
         const char* kp = x.kb + (key0 + lane / CPR) * p.k_l + lane % CPR * 16;
         const char* vp = x.vb + (key0 + lane / CPR) * p.v_l + lane % CPR * 16;
+        if (key0 + TK <= x.hi) {   // (all but a shard's last tile)
 #pragma unroll
-        for (int i = 0; i < TK * CPR / 32; ++i) {
-            const int row = lane / CPR + i * (32 / CPR), ch = lane % CPR;
-            const bool ok = key0 + row < x.hi;
-            cp_async16(st + k_off(row, ch), ok ? kp : x.kb, ok ? 16 : 0);
-            cp_async16(st + kVOff + v_off(row, ch), ok ? vp : x.vb, ok ? 16 : 0);
-            kp += (32 / CPR) * p.k_l;
-            vp += (32 / CPR) * p.v_l;
+            for (int i = 0; i < TK * CPR / 32; ++i) {
+                const int row = lane / CPR + i * (32 / CPR), ch = lane % CPR;
+                cp_async16(st + k_off(row, ch), kp, 16);
+                cp_async16(st + kVOff + v_off(row, ch), vp, 16);
+                kp += (32 / CPR) * p.k_l;
+                vp += (32 / CPR) * p.v_l;
+            }
+        } else {
+#pragma unroll 2
+            for (int i = 0; i < TK * CPR / 32; ++i) {
+                const int row = lane / CPR + i * (32 / CPR), ch = lane % CPR;
+                const bool ok = key0 + row < x.hi;
+                cp_async16(st + k_off(row, ch), ok ? kp : x.kb, ok ? 16 : 0);
+                cp_async16(st + kVOff + v_off(row, ch), ok ? vp : x.vb, ok ? 16 : 0);
+                kp += (32 / CPR) * p.k_l;
+                vp += (32 / CPR) * p.v_l;
+            }
         }
         const bool ok = key0 + lane < x.hi;
         const int64_t key = ok ? key0 + lane : x.lo;
@@ -372,11 +384,17 @@ struct Tiles8 {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const bool ok = key0 + 16 * kk + 4 * t + 2 * h + e < x.hi;
                     float* c = sc[2 * kk + h];
-                    c[e] = ok ? c[e] * (s[2 * h + e] * q.scale0) : -INFINITY;
-                    if (!kRows8) c[e + 2] = ok ? c[e + 2] * (s[2 * h + e] * q.scale1) : -INFINITY;
+                    c[e] *= s[2 * h + e] * q.scale0;
+                    if (!kRows8) c[e + 2] *= s[2 * h + e] * q.scale1;
                 }
+        }
+        if (key0 + TK > x.hi) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (key0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e >= x.hi) sc[j][e] = sc[j][e + 2] = -INFINITY;
         }
         softmax_step<__half, D, NJ, kRows8>(sc, w);
         // the reference of the values' scales: a power of two, only raised
