@@ -33,9 +33,9 @@
 // 103 us, 5.4 TB/s, 82 % of the measured copy rate (97 us where the keys of the call
 // before are partly in L2 still).  Bound by the instructions per key (codes to f16,
 // products that use 4 of 16 rows) and their latencies: two warps per scheduler use 42
-// to 53 % of the issue slots.  With tests in full tiles too: 106.  Three CTAs per SM with two stages each
-// took 112 us (512 CTAs leave a tail), scaling o in every tile and all rows' softmax
-// 119.  One sequence, 16 shards: 9.7 us with the merge, latency.
+// to 53 % of the issue slots.  With tests in full tiles too: 106.  Three CTAs per SM
+// with two stages each took 112 us (512 CTAs leave a tail), scaling o in every tile
+// and all rows' softmax 119.  One sequence, 16 shards: 9.7 us with the merge, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
