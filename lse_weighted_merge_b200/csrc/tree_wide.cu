@@ -183,15 +183,20 @@ struct Lay {
     static constexpr int kBlock = kTK * 128;        // 64 columns of it
     static constexpr int kRaw = kTK * D;            // a tile of codes
     static constexpr int kCtrl = 7 * kTile;
-    static constexpr int kBytes = kCtrl + 256 + 5 * 512;
+    static constexpr int kScales = kCtrl + 384;     // rings of scales, behind the control block
+    static constexpr int kBytes = kScales + 5 * 512;
     // byte offset of 16-byte chunk ch of row
     __device__ static uint32_t at(int row, int ch) {
         return (uint32_t)((ch >> 3) * kBlock + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
     }
 };
 
-// Barriers, 8 bytes each, at the control block: S and P by stream and half.
-enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 17, kODone = 21, kBars = 23 };
+// Barriers, 8 bytes each, at the control block: S, P and the end of a P V by stream
+// and half, the end of all products by stream.  A wait names a phase by its parity, so
+// it must never be made while the phase before is still open: whoever waits for P V of
+// a half knows from S of that half or the next, issued behind them, that the P V of
+// two halves before, the barrier's phase before, is complete.
+enum { kQFull = 0, kKFull = 1, kKEmpty = 4, kVFull = 7, kVEmpty = 10, kSFull = 13, kPFull = 17, kODone = 21, kEnd = 25, kBars = 27 };
 
 struct Ctrl {
     uint64_t bar[kBars];
@@ -203,7 +208,7 @@ struct Ctrl {
     // and whether the tile's values still need theirs
     float4 tile[3];   // by tile: these three
 };
-static_assert(sizeof(Ctrl) <= 256, "control block");
+static_assert(sizeof(Ctrl) <= 384, "control block");
 
 // How a CTA's tiles are laid out in time: the same for all roles.
 struct WidePlan {
@@ -520,7 +525,7 @@ __device__ __forceinline__ void issue(const WidePlan& pl, int s, uint32_t smem_u
 #pragma unroll
         for (int u = 0; u < kHK / 16; ++u)
             mma_ts(tO, tS + (h.seq & 1) * kHK + u * 8, v + (u * 2048 >> 4), kIdPV, h.seq > 0 || u > 0);
-        tc_commit(bars + 8 * (kODone + s));
+        tc_commit(bars + 8 * (kODone + 2 * s + (h.seq & 1)));
         if (h.ends_tile()) tc_commit(bars + 8 * (kVEmpty + slot));
     };
     Halves a(pl, s), b(pl, s);   // of Q K^T and of P V
@@ -533,6 +538,7 @@ __device__ __forceinline__ void issue(const WidePlan& pl, int s, uint32_t smem_u
             a.next();
         }
     }
+    if (b.seq > 0) tc_commit(bars + 8 * (kEnd + s));   // behind all of the stream's products
 }
 
 // ------------------------------------------------------------ queries
@@ -744,7 +750,7 @@ __device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, float vref, 
         st.vref = vref;
     }
     if (__any_sync(kFull, down != 1.f) && seq > 0) {
-        wait(o_done, (uint32_t)(seq - 1) & 1u, dead);   // P V of the half before is in
+        wait(o_done + 8 * ((seq - 1) & 1), (uint32_t)((seq - 1) >> 1) & 1u, dead);   // P V of the half before is in
         tc_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     pl.n = pl.cached + (last_row > row0 && (x.drafts || (p.fold && r == p.R - 1)) ? 1 : 0);
     pl.len = x.hi - x.lo, pl.live = x.live;
     // the scales' rings: keys' by tile, values' by slot
-    float* ks = reinterpret_cast<float*>(smem + L::kCtrl + 256);
+    float* ks = reinterpret_cast<float*>(smem + L::kScales);
     float* vs = ks + 3 * kTK;
     if (tid == 0) {
         auto init = [&](int b, int n) {
@@ -803,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             init(kVFull + i, kLoadWarps), init(kVEmpty + i, users);
         }
         for (int i = 0; i < 4; ++i) init(kSFull + i, 1), init(kPFull + i, 4);
-        for (int s = 0; s < 2; ++s) init(kODone + s, 1);
+        for (int i = 0; i < 4; ++i) init(kODone + i, 1);
+        for (int s = 0; s < 2; ++s) init(kEnd + s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ctrl->dead = (smem_u & 1023u) != 0;   // the swizzle's atoms are 1024 bytes
         ctrl->bad = 0;
@@ -882,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
                         sc.vinv = pow2_inverse(vref);
                         __syncwarp();
                     }
-                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + s), seq, &ctrl->dead, ready, st);
+                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + 2 * s), seq, &ctrl->dead, ready, st);
                 }
                 tc_before();
                 __syncwarp();
@@ -891,11 +898,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             kslot += step;
             if (kslot >= 3) kslot -= 3;
         }
-        const int last = seq - 1;   // the last P V
-        if (last >= 0) wait(bars + 8 * (kODone + s), (uint32_t)last & 1u, &ctrl->dead);
+        if (seq > 0) wait(bars + 8 * (kEnd + s), 0, &ctrl->dead);
         if (ctrl->dead) {   // what was issued has to be complete before TMEM is freed
             const int64_t t0 = clock64();
-            while (last >= 0 && !try_wait(bars + 8 * (kODone + s), (uint32_t)last & 1u) && clock64() - t0 < kGiveUpClocks) {
+            while (seq > 0 && !try_wait(bars + 8 * (kEnd + s), 0) && clock64() - t0 < kGiveUpClocks) {
             }
         }
         tc_after();
