@@ -332,6 +332,7 @@ int lse_merge_kv_dequantize(const lse_merge_kv_args* args, lse_merge_stream_t st
  *   tree         int64 [B, T] (row stride tree_b; 0 = the same tree for all)
  *   out_o        dense [B, T, Hq, D] of out_dtype; out_lse dense [B, T, Hq] fp32
  *   dtype        LSE_MERGE_BF16 or LSE_MERGE_F16;  1 <= T <= 64;  D 64 or 128;
+ *                1 <= L <= 2^31 - 1025 (an empty cache is kv_len 0);
  *                Hq a multiple of Hkv with Hq / Hkv <= 16
  *   R            shards the cache is cut into (ceil(len_b / R) keys each);
  *                partials of the shards are merged by weight

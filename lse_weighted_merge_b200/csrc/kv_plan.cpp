@@ -214,6 +214,9 @@ int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan) {
     if (a.D != 64 && a.D != 128) return LSE_MERGE_EUNSUP;
     if (a.Hq % a.Hkv != 0 || a.Hq / a.Hkv > 16 || a.T > LSE_MERGE_TREE_MAX_T) return LSE_MERGE_EUNSUP;
     if (a.B > 65535 || a.Hkv > 65535 || a.R > 65535) return LSE_MERGE_EDIMS;
+    // 32-bit key indexes run past a shard's end, by up to 351 (the wide kernel's scales,
+    // brought a tile ahead)
+    if (a.L > INT32_MAX - 1024) return LSE_MERGE_EDIMS;
     // row indexes of the merge fit 30 bits
     if ((i128)a.B * a.T * a.Hq > ((i128)1 << 30)) return LSE_MERGE_EDIMS;
     if (!(a.scale == a.scale) || a.scale > 3.0e38f || a.scale < -3.0e38f) return LSE_MERGE_EDIMS;
