@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(256) kv_quantize_kernel(const KvParams p) {
     constexpr int kLanes = D / 16, E = (int)sizeof(T);
     pdl_wait();
     pdl_release();
-    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / kLanes;
+    const uint32_t i = blockIdx.x * (256u / kLanes) + threadIdx.x / kLanes;   // (threads may pass 32 bits, rows do not)
     const int lane = threadIdx.x % kLanes;
     if (i >= p.rows) return;   // whole groups of lanes: the shuffles below stay within one
     int b, h, j;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256) kv_dequantize_kernel(const KvParams p) {
     constexpr int kLanes = D / 16, E = (int)sizeof(T);
     pdl_wait();
     pdl_release();
-    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / kLanes;
+    const uint32_t i = blockIdx.x * (256u / kLanes) + threadIdx.x / kLanes;   // (threads may pass 32 bits, rows do not)
     const int lane = threadIdx.x % kLanes;
     if (i >= p.rows) return;
     int b, h, j;
