@@ -24,9 +24,12 @@
 //     8) consecutive d for P V.
 //     q is scaled per row by a power of two to at most 2^15 (f16 holds what is
 //     left exactly, down to 2^-39 of the row's largest element).  A key's scale
-//     multiplies its score.  A value's scale w multiplies its weight p before
-//     the rounding to f16, relative to a power of two near the largest scale
-//     that the warp has seen.
+//     multiplies its score.  A value's scale s multiplies its weight p before
+//     the rounding to f16, times a power of two per row (the row's gain) that keeps
+//     the largest p * s seen so far, of a value that is not all zeros, at 2^4 or
+//     more.  So what counts is a key's part in the result, not its scale: a row
+//     of zeros (whose scale is 1) or a large value of little weight takes no
+//     precision from the others.  Scales within 2^100 of each other are held.
 //   * Up to 8 rows (a decode step, mostly) leave the products' rows 8 to 15 empty;
 //     nothing but the products is then done for them.
 // Measured on B200, 64 sequences of 4096 e4m3 tokens, 32 heads over 8, D = 128:
@@ -89,11 +92,27 @@ __device__ __forceinline__ float ex2(float x) {   // results below 2^-126 are 0
     return y;
 }
 
+// 2^e; below 2^-126: 0.
+__device__ __forceinline__ float pow2_of(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+
+// e4m3: the powers of two by which the weights of rows g and g + 8, times their values'
+// scales, are multiplied before they are rounded: o is that much larger.  As large as
+// can be until the row has met a value.  top: the largest exponent of a scale so far.
+constexpr float kTopGain = 8.507059e37f;   // 2^126
+struct Gain {
+    float a = kTopGain, b = kTopGain;
+    int top = -128;
+};
+
 // Fold the tile's scores (C layout, log2 units, -inf where not seen) into the
 // running sums: on return sc holds the weights exp2(s - reference).  A row without
-// any key so far keeps m = -inf, sums 0.  kRows8: there are no rows g + 8.
-template <typename TM, int D, int NJ, bool kRows8>
-__device__ __forceinline__ void softmax_step(float (&sc)[NJ][4], RowState<D>& w) {
+// any key so far keeps m = -inf, sums 0.  kRows8: there are no rows g + 8.  kGain (an
+// e4m3 cache): where the reference rises by 2^k, the gain does in place of o falling, so
+// that o stays relative to its largest parts.  Returns, for the whole warp, whether a
+// score lies more than high0 (rows g) or high1 above its reference.
+template <typename TM, int D, int NJ, bool kRows8, bool kGain>
+__device__ __forceinline__ bool softmax_step(float (&sc)[NJ][4], RowState<D>& w, Gain& gain, float high0, float high1) {
     using Ref = Reference<TM>;
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -101,21 +120,37 @@ __device__ __forceinline__ void softmax_step(float (&sc)[NJ][4], RowState<D>& w)
         mx0 = fmaxf(mx0, fmaxf(sc[j][0], sc[j][1]));
         if (!kRows8) mx1 = fmaxf(mx1, fmaxf(sc[j][2], sc[j][3]));
     }
-    bool move = mx0 - w.m0 > Ref::kHigh;   // (of any lane of the row: NaN, no key, is false)
-    if (!kRows8) move = move || mx1 - w.m1 > Ref::kHigh;
-    if (__any_sync(kFull, move)) {
-        auto raise = [](float mx, float& m, float& l) {
+    bool move = mx0 - w.m0 > high0;   // (of any lane of the row: NaN, no key, is false)
+    if (!kRows8) move = move || mx1 - w.m1 > high1;
+    move = __any_sync(kFull, move);
+    if (move) {
+        auto raise = [](float mx, float& m, float& l, float& up) {
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
             if (!(mx - m > Ref::kHigh)) return 1.f;
-            const float next = mx - Ref::kLow, a = ex2(m - next);   // 0 at first
+            const float next = mx - Ref::kLow;
+            if (kGain) {
+                const float by = ceilf(next - m);   // infinite at first
+                if (!(by <= 252.f)) {
+                    m = next;
+                    l *= 0.f;
+                    up = kTopGain;
+                    return 0.f;
+                }
+                const int k = (int)by, e = exponent(up) + k;
+                m += by;
+                l *= pow2_of(-k);
+                up = pow2_of(min(e, 126));
+                return e > 126 ? pow2_of(126 - e) : 1.f;
+            }
+            const float a = ex2(m - next);   // 0 at first
             m = next;
             l *= a;
             return a;
         };
-        const float a0 = raise(mx0, w.m0, w.l0);
+        const float a0 = raise(mx0, w.m0, w.l0, gain.a);
         float a1 = 1.f;
-        if (!kRows8) a1 = raise(mx1, w.m1, w.l1);
+        if (!kRows8) a1 = raise(mx1, w.m1, w.l1, gain.b);
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
             w.o[n][0] *= a0;
@@ -135,6 +170,7 @@ __device__ __forceinline__ void softmax_step(float (&sc)[NJ][4], RowState<D>& w)
             w.l1 += sc[j][2] + sc[j][3];
         }
     }
+    return move;
 }
 
 // ------------------------------------------------------------ 16-bit tiles
@@ -179,8 +215,7 @@ struct Tiles16 {
     // words: the draft masks of rows g and g + 8 (all ones over a cache).
     __device__ static void attend(const TreeParams& p, const Shard& x, unsigned char* st_p, uint32_t st,
                                   const Query& q, int key0, uint64_t word0, uint64_t word1, int lane,
-                                  RowState<D>& w, float& vref) {
-        (void)vref;
+                                  RowState<D>& w, Gain& gain) {
         const int t = lane & 3;
         float sc[2][4];
 #pragma unroll
@@ -206,7 +241,7 @@ struct Tiles16 {
                 sc[j][e] = ok0 ? sc[j][e] * q.scale0 : -INFINITY;
                 if (!kRows8) sc[j][e + 2] = ok1 ? sc[j][e + 2] * q.scale1 : -INFINITY;
             }
-        softmax_step<T, D, 2, kRows8>(sc, w);
+        softmax_step<T, D, 2, kRows8, false>(sc, w, gain, Reference<T>::kHigh, Reference<T>::kHigh);
         uint32_t pa[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -357,7 +392,7 @@ struct Tiles8 {
     // Column 2t + e of score tile 2 * kk + h is key 16 * kk + 4t + 2h + e.
     __device__ static void attend(const TreeParams& p, const Shard& x, unsigned char* st_p, uint32_t st,
                                   const Query& q, int key0, uint64_t, uint64_t, int lane,
-                                  RowState<D>& w, float& vref) {
+                                  RowState<D>& w, Gain& gain) {
         constexpr int NJ = TK / 8;
         const int g = lane >> 2, t = lane & 3;
         float sc[NJ][4];
@@ -375,7 +410,7 @@ struct Tiles8 {
             }
         }
         const float* ks = reinterpret_cast<const float*>(st_p + kSOff);
-        const float* vs = ks + TK;
+        float* vs = reinterpret_cast<float*>(st_p + kSOff) + TK;
 #pragma unroll
         for (int kk = 0; kk < TK / 16; ++kk) {
             const float4 s4 = *reinterpret_cast<const float4*>(ks + 16 * kk + 4 * t);
@@ -396,31 +431,78 @@ struct Tiles8 {
                 for (int e = 0; e < 2; ++e)
                     if (key0 + 16 * (j >> 1) + 4 * t + 2 * (j & 1) + e >= x.hi) sc[j][e] = sc[j][e + 2] = -INFINITY;
         }
-        softmax_step<__half, D, NJ, kRows8>(sc, w);
-        // the reference of the values' scales: a power of two, only raised
-        const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs[lane])));
-        const float ref = fmaxf(vref, pow2_below(top));
-        if (ref != vref) {
-            const float down = vref * pow2_inverse(ref);   // 0 at first, when o is 0
+        // A weight times its value's scale and the gain stays below 2^16 where the row's
+        // largest score and the tile's largest scale say so.
+        using Ref = Reference<__half>;
+        const int top = exponent(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs[lane]))));
+        const float high0 = fminf(Ref::kHigh, 14.99f - (float)(top + exponent(gain.a)));
+        const float high1 = fminf(Ref::kHigh, 14.99f - (float)(top + exponent(gain.b)));
+        const bool near = softmax_step<__half, D, NJ, kRows8, true>(sc, w, gain, high0, high1) || top > gain.top;
+        const bool first = gain.top == -128;
+        gain.top = max(gain.top, top);
+        if (near) {
+            // Values that are all zeros do not count.
+            uint32_t code = 0;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                w.o[n][0] *= down;
-                w.o[n][1] *= down;
-                if (!kRows8) w.o[n][2] *= down, w.o[n][3] *= down;
+            for (int i = 0; i < CPR; ++i) {   // (from another chunk in each lane: other banks)
+                const uint4 y = *reinterpret_cast<const uint4*>(st_p + kVOff + v_off(lane, (lane + i) % CPR));
+                code |= y.x | y.y | y.z | y.w;
             }
-            vref = ref;
+            const float mine = vs[lane];
+            const bool none = (code & 0x7f7f7f7fu) == 0;
+            const int low = exponent(__uint_as_float(__reduce_min_sync(kFull, __float_as_uint(mine) - 1) + 1));   // (not absent keys' 0)
+            if (first && !__any_sync(kFull, none && mine != 0.f) && top - low <= 3 && top > -127 && top < 127) {
+                // The largest weight is 2^7 here, the largest product 2^4 to 2^8 at this gain:
+                // good enough, and 1 us less for one sequence's call than the steps below.
+                gain.a = gain.b = pow2_of(-top);
+            } else {
+                // A row whose largest product is too large lowers its gain.
+                if (none) vs[lane] = 0.f;
+                __syncwarp();
+                float mx0 = 0.f, mx1 = 0.f;   // the largest products, times 2^-15
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float s = vs[16 * (j >> 1) + 4 * t + 2 * (j & 1) + e] * 3.0517578e-05f;
+                        mx0 = fmaxf(mx0, sc[j][e] * s);
+                        if (!kRows8) mx1 = fmaxf(mx1, sc[j][e + 2] * s);
+                    }
+                // (a scale times the gain stays finite: a weight of 0 times it is 0)
+                const float most = pow2_of(min(100 - gain.top, 126));
+                auto lower = [most](float mx, float& up) {
+                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+                    float next = up;
+                    // (65504 = 1.999 * 2^15; the largest product becomes 2^7 to 2^8)
+                    if (mx * up > 1.9989f) next = fmaxf(pow2_inverse(pow2_below(mx)) * 0.00390625f, 1.17549435e-38f);
+                    next = fminf(next, most);
+                    const float down = next * pow2_inverse(up);
+                    up = next;
+                    return down;
+                };
+                const float d0 = lower(mx0, gain.a);
+                float d1 = 1.f;
+                if (!kRows8) d1 = lower(mx1, gain.b);
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    w.o[n][0] *= d0;
+                    w.o[n][1] *= d0;
+                    if (!kRows8) w.o[n][2] *= d1, w.o[n][3] *= d1;
+                }
+            }
         }
-        const float inv = pow2_inverse(ref);
 #pragma unroll
         for (int kk = 0; kk < TK / 16; ++kk) {
             const float4 s4 = *reinterpret_cast<const float4*>(vs + 16 * kk + 4 * t);
-            const float s[4] = {s4.x * inv, s4.y * inv, s4.z * inv, s4.w * inv};
+            const float s[4] = {s4.x, s4.y, s4.z, s4.w};
             uint32_t pa[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float* c = sc[2 * kk + h];
-                pa[2 * h] = Mma<__half>::pack(c[0] * s[2 * h], c[1] * s[2 * h + 1]);
-                pa[2 * h + 1] = kRows8 ? 0u : Mma<__half>::pack(c[2] * s[2 * h], c[3] * s[2 * h + 1]);
+                pa[2 * h] = Mma<__half>::pack(c[0] * (s[2 * h] * gain.a), c[1] * (s[2 * h + 1] * gain.a));
+                pa[2 * h + 1] = 0u;
+                if (!kRows8) pa[2 * h + 1] = Mma<__half>::pack(c[2] * (s[2 * h] * gain.b), c[3] * (s[2 * h + 1] * gain.b));
             }
             // keys 4t .. 4t + 3 of this step at D / 8 consecutive d from g * D / 8
             uint32_t u[4][D / 32];
@@ -460,7 +542,7 @@ __device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x
     const uint32_t ring_u = smem_u32(ring);
     const int g = lane >> 2, t = lane & 3;
     w.reset();
-    float vref = 0.f;
+    Gain gain;
     const int ntiles = (x.hi - x.lo + TK - 1) / TK;
     const int mine = ntiles > warp ? (ntiles - warp + kRowWarps - 1) / kRowWarps : 0;
 #pragma unroll
@@ -485,7 +567,7 @@ __device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x
         cp_wait<S - 1>();
         __syncwarp();
         Tiles::attend(p, x, ring + (i % S) * Tiles::kBytes, ring_u + (i % S) * Tiles::kBytes, q,
-                      x.lo + (warp + i * kRowWarps) * TK, word0, word1, lane, w, vref);
+                      x.lo + (warp + i * kRowWarps) * TK, word0, word1, lane, w, gain);
         __syncwarp();
     }
     cp_wait<0>();
@@ -494,12 +576,13 @@ __device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x
     w.l1 += __shfl_xor_sync(kFull, w.l1, 1);
     w.l1 += __shfl_xor_sync(kFull, w.l1, 2);
     if (Tiles::TK == 32) {
+        const float down0 = pow2_inverse(gain.a), down1 = pow2_inverse(gain.b);
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
-            w.o[n][0] *= vref;
-            w.o[n][1] *= vref;
-            w.o[n][2] *= vref;
-            w.o[n][3] *= vref;
+            w.o[n][0] *= down0;
+            w.o[n][1] *= down0;
+            w.o[n][2] *= down1;
+            w.o[n][3] *= down1;
         }
     }
 }
