@@ -23,8 +23,13 @@
 // the last shard, the only one with a mask row by row.  e4m3 tiles come by cp.async
 // as they are; each warp converts what it fetched to f16 (exact) and stores it
 // swizzled.  q is scaled per row by a power of two.  Scales that are powers of two
-// (as lse_merge_kv_quantize writes them) go into the f16 tiles, exactly; others
-// multiply scores and weights one by one.  The drafts of an e4m3 cache, whose
+// (as lse_merge_kv_quantize writes them) and near each other go into the f16 tiles,
+// exactly; others multiply scores and weights one by one.  The values' scales are
+// relative to a unit that changes where a tile's scales do not fit it; values that are
+// all zeros (whose scale is 1) do not count.  Weights of a tile whose values' scales lie
+// far apart are rounded with their scales, relative to the largest such product, so that
+// a large value of little weight takes no precision from the others.  (Values up to
+// 2^70 apart in one call are held.)  The drafts of an e4m3 cache, whose
 // products are of another type, are a launch of their own; a lone cached shard
 // joins their partial.  Weights are rounded to the tiles' type (a tensor core product
 // takes one type: f16 for e4m3 and f16 caches, bf16 for a bf16 one), their sums are
@@ -61,7 +66,7 @@ constexpr int kLoadWarps = 8;
 constexpr int kThreads = (8 + kLoadWarps + 4) * 32;
 // Registers per thread of the softmax, loading and issuing warps: together at most
 // what the block is launched with.
-constexpr int kSoftRegs = 144, kLoadRegs = 72, kIssueRegs = 40, kLaunchRegs = 96;
+constexpr int kSoftRegs = 144, kLoadRegs = 80, kIssueRegs = 32, kLaunchRegs = 96;
 static_assert(256 * kSoftRegs + kLoadWarps * 32 * kLoadRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs &&
               kThreads * kLaunchRegs <= 65536 && kThreads * (kLaunchRegs + 8) > 65536, "registers");
 constexpr int kTK = 128;                    // keys per tile
@@ -147,6 +152,16 @@ __device__ __forceinline__ void tm_put32(uint32_t at, const float (&f)[32]) {
         LSEM_OP32("f", f)
         : "memory");
 }
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 lds2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
 // One thread of the (converged) warp, in a form that lets the branch be uniform.
 __device__ __forceinline__ bool elect() {
     uint32_t yes;
@@ -203,12 +218,19 @@ struct Ctrl {
     uint32_t tmem;
     int dead;
     int bad;            // a value of the drafts is no number
-    // e4m3, known with a tile's keys: the power of two that these were scaled by
-    // (0: their scores still need the scales), the reference of the values' scales,
-    // and whether the tile's values still need theirs
-    float4 tile[3];   // by tile: these three
+    // e4m3, known with a tile's keys: the power of two that the values are relative to,
+    // the Values they are, and the power of two that the keys were scaled by (0: their
+    // scores still need the scales); by tile, these three
+    float4 tile[3];
 };
 static_assert(sizeof(Ctrl) <= 384, "control block");
+
+// e4m3: the values of a tile are codes times scale / unit, or codes whose scales (at most
+// 2 units) multiply the weights, or all zeros.
+enum Values { kScaled = 0, kCodes = 1, kZeros = 2 };
+// The scales that go into the tile are powers of two in [unit * kFloor, unit * kCeil]: f16
+// has codes times these exactly, and weights alone, rounded to f16, are precise enough.
+constexpr float kFloor = 0.00390625f, kCeil = 128.f;
 
 // How a CTA's tiles are laid out in time: the same for all roles.
 struct WidePlan {
@@ -444,33 +466,69 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         fetch(v, raw(1, j), j < pl.n);
     }
     Ring kr{2, 0, 1}, vr{2, 0, 1};
-    float run = 1.17549435e-38f;   // the reference of the values' scales
+    float base = 0.f, unit = 1.f;   // what scaled values are relative to, this tile's
     Scales sk{p.ks + x.b * p.ks_b + x.hk * p.ks_h + (x.lo + lane) * p.ks_l, p.ks_l, x.lo + lane, {}};
     Scales sv{p.vs + x.b * p.vs_b + x.hk * p.vs_h + (x.lo + lane) * p.vs_l, p.vs_l, x.lo + lane, {}};
     sk.next(x.hi);
     sv.next(x.hi);
     int kslot = 0;
     // the first warp keeps the scales that are not in the tile
-    auto keep = [&](float* at, const Scales& sc) {
+    auto keep = [&](float* at, const Scales& sc, float inv) {
         if (warp != 0) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) at[lane + 32 * e] = sc.v[e];
+        for (int e = 0; e < 4; ++e) at[lane + 32 * e] = sc.v[e] * inv;
     };
     for (int j = 0; j < pl.n; ++j) {
         // f16 has codes * 2^-15 .. 1 exactly: scales that are powers of two go into the tile
         float kbig, vbig, small;
         bool kplain = sk.survey(kbig, small);
         kplain = kplain && small >= kbig * 3.0517578e-05f && kbig >= 1.17549435e-38f && kbig <= 8.507059e37f;
-        bool vplain = sv.survey(vbig, small);
-        run = fmaxf(run, pow2_below(vbig));
-        vplain = vplain && small >= run * 3.0517578e-05f && small >= 1.17549435e-38f && vbig <= run;
+        bool pow2 = sv.survey(vbig, small);
+        auto fits = [&]() { return pow2 && small >= base * kFloor && vbig <= base * kCeil; };
+        auto compact = [&]() { return pow2 && small >= vbig * kFloor && vbig >= 7.7037198e-34f && vbig <= 1.2980742e33f; };
+        int form = kScaled;
+        if (vbig == 0.f || !fits()) {
+            // Values that are all zeros do not count: of those whose scales stand out (in the
+            // first tile, those of 1 as well, which lse_merge_kv_quantize gives them), every
+            // warp looks at the codes (for itself: it happens seldom).
+            const float low = base * kFloor, high = fminf(base != 0.f ? base * kCeil : 0.999f, small / kFloor);
+            if (vbig > high || small < low) {
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    float mine = sv.v[0];
+                    if (mine > high || (mine < low && mine != 0.f)) {
+                        const char* at = x.vb + (int64_t)(x.lo + j * kTK + lane + 32 * e) * p.v_l;
+                        uint32_t code = 0;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            const uint4 y = __ldcg(reinterpret_cast<const uint4*>(at) + c);
+                            code |= y.x | y.y | y.z | y.w;
+                        }
+                        if ((code & 0x7f7f7f7fu) == 0) mine = 0.f;
+                    }
+                    sv.v[0] = sv.v[1], sv.v[1] = sv.v[2], sv.v[2] = sv.v[3], sv.v[3] = mine;
+                }
+                __syncwarp();
+                pow2 = sv.survey(vbig, small);
+            }
+            if (vbig == 0.f)
+                form = kZeros;
+            else if (!fits()) {
+                if (compact())
+                    base = vbig;
+                else
+                    form = kCodes;
+            }
+        }
+        if (form == kScaled) unit = base;
+        if (form == kCodes && !(vbig < 2.f * unit && vbig >= 0.0625f * unit)) unit = pow2_below(vbig);
         landed();
         wait(bars + 8 * (kKEmpty + kr.slot), kr.phase, &ctrl->dead);
         convert(smem + (2 + kr.slot) * L::kTile, raw(0, j), kplain, sk, pow2_inverse(pow2_below(kbig)));
         // (the place of three tiles ago: the values of two tiles ago would not be
         // in if that tile's softmax were not over)
-        if (!kplain) keep(ks + kslot * kTK, sk);
-        if (tid == 0) ctrl->tile[kslot] = make_float4(kplain ? kbig : 0.f, run, vplain ? 0.f : 1.f, 0.f);
+        if (!kplain) keep(ks + kslot * kTK, sk, 1.f);
+        if (tid == 0) ctrl->tile[kslot] = make_float4(unit, (float)form, kplain ? kbig : 0.f, 0.f);
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * (kKFull + kr.slot));
         kr.next();
@@ -479,8 +537,8 @@ __device__ __forceinline__ void load8(const TreeParams& p, const Shard& x, const
         fetch(k, raw(0, j), j + ahead < pl.n);
         landed();
         wait(bars + 8 * (kVEmpty + vr.slot), vr.phase, &ctrl->dead);
-        convert(smem + (4 + vr.slot) * L::kTile, raw(1, j), vplain, sv, pow2_inverse(run));
-        if (!vplain) keep(vs + vr.slot * kTK, sv);
+        convert(smem + (4 + vr.slot) * L::kTile, raw(1, j), form == kScaled, sv, pow2_inverse(unit));
+        if (form == kCodes) keep(vs + vr.slot * kTK, sv, pow2_inverse(unit));
         __syncwarp();
         if (lane == 0) arrive(bars + 8 * (kVFull + vr.slot));
         vr.next();
@@ -588,15 +646,19 @@ __device__ __forceinline__ void load_queries(const char* src, unsigned char* til
 
 // ------------------------------------------------------------ softmax
 
-// A row's running state: reference (log2 units), sum of weights, and e4m3: the
-// values' scale that O is relative to.
+// A row's running state: reference (log2 units), sum of weights, and e4m3: the gain of
+// O, which is the sum of weight * scale * code * gain (0: none yet), and the largest
+// weight * scale * gain so far.  The gain is 1 / unit of the tile: weights go into the
+// product as they are, or times scale / unit.  Only where the latter are all below 2^3,
+// so far and in this half, is it larger.  O is scaled where the gain changes.
 struct RowSum {
-    float m, l, vref;
+    float m, l, gain, peak;
 };
+constexpr float kMostPeak = 3.0948501e26f;   // 2^88: O, up to 2^36 times that, stays finite
 // Weights are watched as the largest sum of 4 of them.  A row's first reference
 // lies kLow below its maximum.  Where the sum is past kHigh the reference rises by
 // a power of two that leaves it at 2^kBase to 2^(kBase + 1), the largest weight at
-// a quarter of that or more.  f16 weights so stay between 2^7 (which keeps 2^-24 of
+// a quarter of that or more.  f16 weights so stay between 2^7 (which keeps 2^-21 of
 // the largest at f16's 11 bits) and f16's 65504, a value's scale below 2 included.
 template <typename TM>
 struct Bounds {
@@ -610,8 +672,9 @@ struct Scores {
     uint32_t at;
     float scale;             // of the row (and of all keys of the tile)
     bool each;               // not all are seen, or their scales differ
-    const float4 *k4, *v4;   // e4m3 whose scales are not in the tiles: the keys' (or NULL), the values' (or NULL)
-    float vinv;              // what the values' are multiplied by
+    // e4m3, shared-memory addresses: the scales of keys and of values that are not in the
+    // tiles (or 0), and the tile's unit and Values
+    uint32_t k4, v4, values;
     uint64_t see;
 };
 
@@ -627,7 +690,7 @@ __device__ __forceinline__ void scale_scores(Scores& x) {
         for (int u = 0; u < 32; u += 4) {
             float k[4] = {x.scale, x.scale, x.scale, x.scale};
             if (kFp8 && x.k4) {
-                const float4 s = x.k4[(c + u) / 4];
+                const float4 s = lds4(x.k4 + (c + u) * 4);
                 k[0] *= s.x, k[1] *= s.y, k[2] *= s.z, k[3] *= s.w;
             }
 #pragma unroll
@@ -691,7 +754,7 @@ __device__ __forceinline__ void weigh(float (&f)[64], float scale, float ref, fl
 // reference.  The rare steps are short loops over TMEM, so that the instructions of
 // all halves stay near.
 template <typename TM, int D, bool kFp8>
-__device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, float vref, uint32_t o_done, int seq,
+__device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, uint32_t o_done, int seq,
                                              volatile int* dead, bool& ready, RowSum& st) {
     using Bd = Bounds<TM>;
     float f[64], l, top, down = 1.f;
@@ -733,22 +796,58 @@ __device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, float vref, 
         }
     }
     if constexpr (kFp8) {
+        const float2 values = lds2(x.values);   // (once more: registers are scarce)
+        const float g = pow2_inverse(values.x);
+        float most = top;
         if (x.v4) {
+            most = 0.f;
 #pragma unroll
             for (int u = 0; u < 64; u += 4) {
-                const float4 v = x.v4[u / 4];
-                f[u] *= v.x * x.vinv, f[u + 1] *= v.y * x.vinv, f[u + 2] *= v.z * x.vinv, f[u + 3] *= v.w * x.vinv;
+                const float4 v = lds4(x.v4 + u * 4);
+                f[u] *= v.x, f[u + 1] *= v.y, f[u + 2] *= v.z, f[u + 3] *= v.w;
+                most = fmaxf(fmaxf(most, fmaxf(f[u], f[u + 1])), fmaxf(f[u + 2], f[u + 3]));
             }
         }
+        if (x.v4 || !__all_sync(kFull, st.gain == g)) {
+            const float h = st.gain == 0.f ? 1.f : g * pow2_inverse(st.gain);
+            const float was = st.peak * down * h;   // what O's largest part is at gain g
+            float more = 1.f;
+            if (values.y == (float)kZeros) {
+                most = 0.f;
+            } else if (was <= kMostPeak) {
+                const float row = fmaxf(was, most);
+                if (x.v4 && row < 8.f && row > 0.f)
+                    more = fminf(512.f * pow2_inverse(pow2_below(row)), 1.3292280e36f * pow2_inverse(g));
+                down *= h * more;
+                st.gain = g * more;
+            } else {   // next to nothing beside what O has: left out
+                more = 0.f;
+            }
+            most *= more;
+            if (__any_sync(kFull, more != 1.f)) {
+                tm_put32(x.at, fa);
+                tm_put32(x.at + 32, fb);
+#pragma unroll 1
+                for (int c = 0; c < kHK; c += 32) {
+                    tm_wait_st();
+                    tm_ld32(x.at + c, fa);
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) fa[u] *= more;
+                    tm_put32(x.at + c, fa);
+                }
+                tm_wait_st();
+                tm_get32(x.at, fa);
+                tm_get32(x.at + 32, fb);
+                tm_wait32(fa);
+                tm_wait32(fb);
+            }
+        }
+        st.peak = fmaxf(st.peak * down, most);
     }
 #pragma unroll
     for (int u = 0; u < 32; ++u) f[u] = __uint_as_float(Mma<TM>::pack(f[2 * u], f[2 * u + 1]));
     tm_put32(x.at, fa);
     st.l += l;
-    if (kFp8 && vref != st.vref) {
-        down *= st.vref * pow2_inverse(vref);
-        st.vref = vref;
-    }
     if (__any_sync(kFull, down != 1.f) && seq > 0) {
         wait(o_done + 8 * ((seq - 1) & 1), (uint32_t)((seq - 1) >> 1) & 1u, dead);   // P V of the half before is in
         tc_after();
@@ -823,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
     const int s = warp >> 2 & 1;                        // softmax warps: the stream
     const int row = row0 + (pl.two ? 128 * s : 0) + (tid & 127);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's lanes of TMEM
-    RowSum st{-INFINITY, 0.f, 1.17549435e-38f};
+    RowSum st{-INFINITY, 0.f, 0.f, 0.f};
     uint64_t word = 0;
 
     if (warp >= 8 + kLoadWarps) {
@@ -846,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             const char* src = row < last_row ? q_row(p, x.b, x.hk, row) : nullptr;
             load_queries<T, D, kFp8>(src, pl.two || s == 0 ? smem + (pl.two ? s : 0) * L::kTile : nullptr,
                                      (warp & 3) * 32, lane, p.scale_log2 < 0.f, scale);
-            if ((p.fold || x.drafts) && src) word = (uint64_t)__ldcg(p.tree + x.b * p.tree_b + row / p.G);
+            if (!kFp8 && (p.fold || x.drafts) && src) word = (uint64_t)__ldcg(p.tree + x.b * p.tree_b + row / p.G);
         }
         fence_async();
         __syncwarp();
@@ -859,37 +958,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         bool ready = false;   // all rows of the warp have a reference
         for (int i = 0; i < count; ++i) {
             const int j = pl.tile(s, i), keys = pl.keys(j);
-            float tile_scale = scale, vref = 1.f;
-            float4 info = make_float4(1.f, 1.f, 0.f, 0.f);
+            float tile_scale = scale;
 #pragma unroll 1
             for (int half = 0; half * kHK < keys; ++half, ++seq) {
                 const int buf = seq & 1;
                 wait(s_full + 8 * buf, (uint32_t)(seq >> 1) & 1u, &ctrl->dead);
                 tc_after();
                 if (!idle) {
-                    if (kFp8 && half == 0) {
-                        info = ctrl->tile[kslot];
-                        vref = info.y;
-                        tile_scale = scale * info.x;
+                    float4 info = make_float4(0.f, 0.f, 1.f, 0.f);
+                    if constexpr (kFp8) {
+                        info = lds4(smem_u32(&ctrl->tile[kslot]));
+                        tile_scale = scale * info.z;
                     }
                     const int left = keys - half * kHK;
-                    Scores sc{tS + buf * kHK, tile_scale, left < kHK || j >= pl.cached, nullptr, nullptr, 0.f, ~0ull};
+                    Scores sc{tS + buf * kHK, tile_scale, left < kHK || (!kFp8 && j >= pl.cached), 0, 0, smem_u32(&ctrl->tile[kslot]), ~0ull};
                     if (sc.each) {
                         if (left < kHK) sc.see = (1ull << left) - 1;
-                        if (j >= pl.cached) sc.see &= word;
+                        if (!kFp8 && j >= pl.cached) sc.see &= word;
                     }
-                    if (kFp8 && info.x == 0.f) {
+                    if (kFp8 && info.z == 0.f) {
                         sc.scale = scale;
-                        sc.k4 = reinterpret_cast<const float4*>(ks + kslot * kTK + half * kHK);
+                        sc.k4 = smem_u32(ks + kslot * kTK + half * kHK);
                         sc.each = true;
                     }
-                    if (kFp8 && info.z != 0.f) {
+                    if (kFp8 && info.y == (float)kCodes) {
                         wait(bars + 8 * (kVFull + j % 2), (uint32_t)(j / 2) & 1u, &ctrl->dead);   // their scales
-                        sc.v4 = reinterpret_cast<const float4*>(vs + j % 2 * kTK + half * kHK);
-                        sc.vinv = pow2_inverse(vref);
+                        sc.v4 = smem_u32(vs + j % 2 * kTK + half * kHK);
                         __syncwarp();
                     }
-                    softmax_half<TM, D, kFp8>(sc, tO, vref, bars + 8 * (kODone + 2 * s), seq, &ctrl->dead, ready, st);
+                    softmax_half<TM, D, kFp8>(sc, tO, bars + 8 * (kODone + 2 * s), seq, &ctrl->dead, ready, st);
                 }
                 tc_before();
                 __syncwarp();
@@ -921,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         }
         other[D * 128 + (tid & 127)] = st.m;
         other[(D + 1) * 128 + (tid & 127)] = st.l;
-        other[(D + 2) * 128 + (tid & 127)] = st.vref;
+        other[(D + 2) * 128 + (tid & 127)] = st.gain;
     }
     soft_sync();
     const bool dead = ctrl->dead != 0;
@@ -938,9 +1035,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
             a0 = st.m == -INFINITY ? 1.f : ex2(st.m - ref);   // (a stream that saw no key has sums 0, or NaN)
             a1 = m1 == -INFINITY ? 1.f : ex2(m1 - ref);
             den = a0 * st.l + a1 * l1;
-            if (kFp8) a1 *= other[(D + 2) * 128 + tid];
+            const float gain = other[(D + 2) * 128 + tid];
+            if (kFp8 && gain != 0.f) a1 /= gain;
         }
-        if (kFp8) a0 *= st.vref;
+        if (kFp8 && st.gain != 0.f) a0 /= st.gain;
         if (pl.n == 0) den = 0.f;
         bool any = den != 0.f;   // NaN where a score was
         if (row >= last_row) any = false;
@@ -948,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeParams
         float lse = any ? (M + log2f(den)) * kLn2 : -INFINITY;
         if (dead) any = true, inv = lse = __uint_as_float(0x7fc00000u);
         if (dead && tid == 0) atomicAdd(&g_gave_up, 1u);
-        const bool bad = ctrl->bad != 0 && pl.n > pl.cached;
+        const bool bad = !kFp8 && ctrl->bad != 0 && pl.n > pl.cached;
         const int t = row / p.G;
         const int64_t at = ((int64_t)x.b * p.T + t) * p.Hq + x.hk * p.G + (row - t * p.G);
         const bool store = row < rows;

@@ -7,7 +7,13 @@ largest value, whatever its weight) replaced: with W = max_j p_j max_d |v_jd|,
 A product p_j s_j below f16's normal range is off by 2^-25 at most.  The row's largest
 product, of a value that is not all zeros, was 2^4 or more when the row's gain was last
 set, and the largest code of its value is at least 224 (as kv_quantize_ writes it): each
-key's error is at most 2^-29 of that product times 448, or 2^-28 W."""
+key's error is at most 2^-29 of that product times 448, or 2^-28 W.
+
+More than 16 rows per KV head, the last term: n (2^-27 W + 2^-31 p_max V).  A product that
+is rounded with its scale was 2^3 or more at the row's largest, so 2^-27 as above.  A tile
+whose scales are within 2^15 of each other has them in its values, exactly, and rounds
+weights alone, of which the row's largest is 2^7 or more: 2^-32 p_max |v_j| each, with |v_j|
+at most V, the largest of all or 2^16 times the smallest that is not zeros."""
 import math
 
 import pytest
@@ -22,12 +28,12 @@ KINDS8 = ["bf16+e4m3", "f16+e4m3"]
 
 
 def weighted(q, k, v, scale=None):
-    """max over the keys of p_j max_d |v_jd|, [B, T, Hq], in 64 bits."""
+    """max over the keys of p_j max_d |v_jd|, and of p_j, [B, T, Hq], in 64 bits."""
     B, T, Hq, D = q.shape
     Hkv = k.shape[1]
     x = torch.einsum("bthgd,bhjd->bthgj", q.double().reshape(B, T, Hkv, Hq // Hkv, D), k)
     p = torch.softmax(x * (1 / math.sqrt(D) if scale is None else scale), -1)
-    return (p * v.abs().amax(-1)[:, None, :, None]).amax(-1).reshape(B, T, Hq)
+    return [(p * f).amax(-1).reshape(B, T, Hq) for f in (v.abs().amax(-1)[:, None, :, None], 1.0)]
 
 
 def check_weighted(c, what="", scale=None, **kw):
@@ -37,8 +43,13 @@ def check_weighted(c, what="", scale=None, **kw):
     out, lse, A, S, n, _ = attention(c.q, k, v, scale=scale)
     D = out.shape[-1]
     w = 2 * ((D + 8) * 2.0 ** -23 * S + 2.0 ** -21 + n * 2.0 ** -23)
-    W = weighted(c.q, k, v, scale)
-    bound = U[torch.float32] * out.abs() + (U[torch.float16] + w)[..., None] * A + (n * 2.0 ** -28 * W)[..., None]
+    W, p = weighted(c.q, k, v, scale)
+    last = 2.0 ** -28 * W
+    if c.q.shape[1] * c.q.shape[2] // k.shape[1] > 16:
+        size = v.abs().amax(-1)
+        V = min(float(size.max()), 2.0 ** 16 * float(size[size > 0].min())) if bool((size > 0).any()) else 0.0
+        last = 2.0 ** -27 * W + 2.0 ** -31 * p * V
+    bound = U[torch.float32] * out.abs() + (U[torch.float16] + w)[..., None] * A + (n * last)[..., None]
     worst = float(((got.double() - out).abs() / bound.clamp(min=1e-300)).max())
     assert worst <= 1, f"{what}: error {worst:.3f} of its bound"
     lworst = float(((gl.double() - lse).abs() / (w + 2.0 ** -21 * (1 + lse.abs()))).max())
@@ -58,7 +69,7 @@ def zero_values(c, where):
     c.scales["v_scale"][:, :, where] = 1.0
 
 
-ROWS = [1, 2, 4]       # T of 4 heads per group: 4, 8 and 16 rows
+ROWS = [1, 2, 4, 8, 24, 64]       # T of 4 heads per group: 4, 8, 16 rows; 32, 96, 256
 ZEROS = {"first": [0], "last": [-1], "many": list(range(5, 700, 9)), "a tile": list(range(128)),
          "later tiles": list(range(256, 512)), "the start": list(range(300))}
 
