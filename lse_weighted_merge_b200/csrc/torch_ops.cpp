@@ -70,6 +70,14 @@ const void* address(const at::Tensor& t) { return t.const_data_ptr(); }
 template <typename T = void>
 T* addr(const at::Tensor& t) { return static_cast<T*>(const_cast<void*>(address(t))); }
 
+// Of a tensor that the call writes: its own storage (a lazy clone gets it now).
+template <typename T = void>
+T* addr_to_write(const at::Tensor& t) { return static_cast<T*>(t.mutable_data_ptr()); }
+// Autograd sees that the tensor was written.
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Strides of the first three dimensions.
 void strides3(const at::Tensor& t, int64_t* s) {
     const auto st = t.strides();
@@ -154,8 +162,6 @@ void nargs(Py_ssize_t n, Py_ssize_t want) {
 
 void cache_fields(lse_merge_kv_args& a, const at::Tensor& kc, const at::Tensor& vc, const at::Tensor& ks,
                   const at::Tensor& vs) {
-    a.k_cache = addr(kc), a.v_cache = addr(vc);
-    a.k_scale = addr<float>(ks), a.v_scale = addr<float>(vs);
     strides3(kc, &a.k_b);
     strides3(vc, &a.v_b);
     strides3(ks, &a.ks_b);
@@ -191,14 +197,19 @@ PyObject* quantize(PyObject* const* o, Py_ssize_t n) {
     a.count = lengths(count, B, "count");
     if (!start && B) value_error("start must be given");
     if (B == 0 || Hkv == 0 || T == 0 || (S == 0 && select)) return PyLong_FromLong(LSE_MERGE_OK);
+    const c10::cuda::CUDAGuard guard(kc.device());
     cache_fields(a, kc, vc, *ks, *vs);
+    a.k_cache = addr_to_write(kc), a.v_cache = addr_to_write(vc);
+    a.k_scale = addr_to_write<float>(*ks), a.v_scale = addr_to_write<float>(*vs);
     a.k = addr(k), a.v = addr(v);
     strides3(k, &a.kx_b);
     strides3(v, &a.vx_b);
     a.T = as_int(T), a.S = as_int(S);
     a.dtype = dtype_code(k.scalar_type());
-    const c10::cuda::CUDAGuard guard(kc.device());
-    return PyLong_FromLong(launch(lse_merge_kv_quantize, a));
+    const int rc = launch(lse_merge_kv_quantize, a);
+    if (rc == LSE_MERGE_OK)
+        for (const at::Tensor* t : {&kc, &vc, ks, vs}) written(*t);
+    return PyLong_FromLong(rc);
 }
 
 // (k_cache, v_cache, k_scale, v_scale, start, length, count, dtype) -> (k, v) or code
@@ -224,6 +235,8 @@ PyObject* dequantize(PyObject* const* o, Py_ssize_t n) {
     at::Tensor v = at::detail::empty_cuda({B, Hkv, length, D}, dtype, kc.device(), c10::nullopt);
     if (k.numel() != 0) {
         cache_fields(a, kc, vc, *ks, *vs);
+        a.k_cache = addr(kc), a.v_cache = addr(vc);
+        a.k_scale = addr<float>(*ks), a.v_scale = addr<float>(*vs);
         a.k = addr(k), a.v = addr(v);
         a.kx_b = a.vx_b = Hkv * length * D;
         a.kx_h = a.vx_h = length * D;
