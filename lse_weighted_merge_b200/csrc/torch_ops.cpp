@@ -318,13 +318,16 @@ PyObject* attention(PyObject* const* o, Py_ssize_t n) {
     a.kv_len = lengths(klen, B, "kv_len");
     a.draft_len = lengths(dlen, B, "draft_len");
     const c10::cuda::CUDAGuard guard(dev);
+    const bool empty = B == 0 || T == 0;   // no query token: nothing to launch
     int64_t need = 0;
-    const int rc0 = lse_merge_tree_workspace_bytes(a.B, a.T, a.Hq, a.D, a.R, kd != nullptr, &need);
+    const int rc0 = empty ? LSE_MERGE_OK
+                          : lse_merge_tree_workspace_bytes(a.B, a.T, a.Hq, a.D, a.R, kd != nullptr, &need);
     if (rc0 != LSE_MERGE_OK) return PyLong_FromLong(rc0);
     at::Tensor out = decode ? at::detail::empty_cuda({B, Hq, D}, out_dtype, dev, c10::nullopt)
                             : at::detail::empty_cuda({B, T, Hq, D}, out_dtype, dev, c10::nullopt);
     at::Tensor lse = decode ? at::detail::empty_cuda({B, Hq}, at::kFloat, dev, c10::nullopt)
                             : at::detail::empty_cuda({B, T, Hq}, at::kFloat, dev, c10::nullopt);
+    if (empty) return pair(std::move(out), std::move(lse));
     // the workspace is this call's own, freed in the stream's order: calls on
     // other streams, and graphs captured from them, never share one
     c10::DataPtr ws;

@@ -29,15 +29,15 @@ except ImportError as e:
 def kv_quantize_(k_cache, v_cache, k_scale, v_scale, k, v, start, *, count=None, select=None):
     """Write tokens into an e4m3 cache, in place, quantising them on the way.
 
-    k_cache, v_cache: float8_e4m3fn [B, Hkv, L, D]; k_scale, v_scale: float32
-    [B, Hkv, L] (any strides; codes contiguous along D, D 64 or 128).  k, v
-    [B, Hkv, S, D]: float32, float16 or bfloat16, stride 1 along D.  start:
-    int32 [B], the position of each sequence's first token; count: int32 [B],
-    how many of its tokens are written (default all); select: int32 [B, T],
-    which of the S rows of k and v the tokens are (default 0, 1, ..., S - 1), for
-    the accepted path of a drafted tree.  A token whose position lies outside
-    [0, L), or whose select index lies outside [0, S), is not written; every
-    other row of the cache is left as it was.
+    k_cache, v_cache: float8_e4m3fn [B, Hkv, L, D], D 64 or 128, stride 1 along D,
+    the other strides whole multiples of 16 bytes; k_scale, v_scale: float32
+    [B, Hkv, L], any strides.  k, v [B, Hkv, S, D]: float32, float16 or bfloat16,
+    strides as the caches'.  start: int32 [B], the position of each sequence's
+    first token; count: int32 [B], how many of its tokens are written (default
+    all); select: int32 [B, T], which of the S rows of k and v the tokens are
+    (default 0, 1, ..., S - 1), for the accepted path of a drafted tree.  A token
+    whose position lies outside [0, L), or whose select index lies outside [0, S),
+    is not written; every other row of the cache is left as it was.
 
     Each row's scale is the smallest power of two by which its largest finite
     magnitude fits e4m3's 448; elements that are not finite are stored as
@@ -96,7 +96,8 @@ def decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, *, kv_len=None, 
     them (any positive scales do); Hq a multiple of Hkv, at most 16 times; D 64
     or 128; kv_len an optional int32 tensor [B].  The keys are cut into
     ``splits`` shards whose partials are merged by weight (default: enough to
-    fill the GPU).  Returns (out [B, Hq, D], lse [B, Hq]).
+    fill the GPU).  L is 1 or more (an empty cache is kv_len 0).  Returns (out
+    [B, Hq, D], lse [B, Hq]).
     """
     got = _torch_ops.attention(True, q, k_cache, v_cache, None, None, None, k_scale, v_scale, kv_len, None, splits,
                                scale, out_dtype)
@@ -120,9 +121,10 @@ def tree_attention(q, k_cache, v_cache, k_draft=None, v_draft=None, tree=None, *
     gives 0 and -inf.  Without k_draft, v_draft and tree the tokens attend to
     the cache alone (a shard of it, say: the lse merges with others').
 
-    Strides are free but for stride 1 along D; Hq is a multiple of Hkv, at most
-    16 times; D 64 or 128.  ``splits``: shards of the cached keys, whose
-    partials are merged by weight.  Returns (out [B, T, Hq, D], lse [B, T, Hq]).
+    Stride 1 along D, the other strides whole multiples of 16 bytes (scales: any);
+    Hq is a multiple of Hkv, at most 16 times; D 64 or 128; L is 1 or more (an
+    empty cache is kv_len 0); B or T may be 0.  ``splits``: shards of the cached
+    keys, whose partials are merged by weight.  Returns (out [B, T, Hq, D], lse [B, T, Hq]).
     """
     got = _torch_ops.attention(False, q, k_cache, v_cache, k_draft, v_draft, tree, k_scale, v_scale, kv_len,
                                draft_len, splits, scale, out_dtype)

@@ -1,4 +1,4 @@
-"""The 8-bit cache's write as torch sees it: lazy clones and version counters."""
+"""The 8-bit cache as torch sees it: lazy clones, version counters, calls of no tokens."""
 import pytest
 import torch
 
@@ -46,3 +46,20 @@ def test_versions_and_saved_tensors():
         lm.kv_quantize_(*made, k, k, ints([4]))
     lm.kv_quantize_(*made, k, k, st)
     assert torch.equal(made[2][..., 4:6], ks[..., :2])
+
+
+def test_attention_of_no_query_tokens():
+    """A batch of no sequences, and no drafted tokens: results of that size."""
+    (kc, ks), (vc, vs) = (cache(2, 2, 12, 64, i) for i in (1, 2))
+    none = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = lm.decode_attention_fp8(none, kc[:0], vc[:0], ks[:0], vs[:0], kv_len=ints([]), out_dtype=torch.float32)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and out.dtype == torch.float32
+    out, lse = lm.tree_attention(none[:, None].expand(0, 3, 4, 64), kc[:0], vc[:0], k_scale=ks[:0], v_scale=vs[:0])
+    assert out.shape == (0, 3, 4, 64) and lse.shape == (0, 3, 4)
+    q = torch.zeros(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    d = torch.zeros(2, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = lm.tree_attention(q, kc, vc, d, d.clone(), torch.zeros(2, 0, dtype=torch.int64, device="cuda"),
+                                 k_scale=ks, v_scale=vs)
+    assert out.shape == (2, 0, 4, 64) and lse.shape == (2, 0, 4)
+    with pytest.raises(ValueError):
+        lm.decode_attention_fp8(none, kc, vc, ks, vs)
