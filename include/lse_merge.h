@@ -368,7 +368,8 @@ typedef struct {
     int32_t reserved;
 } lse_merge_tree_args;
 
-/* Bytes of the workspace: the partials of R shards (and of the drafts), fp32. */
+/* Bytes of the workspace: the partials of R shards (and of the drafts), fp32; as many as
+ * any head layout and cache type needs at these sizes. */
 int lse_merge_tree_workspace_bytes(int B, int T, int Hq, int D, int R, int drafts, int64_t* bytes);
 int lse_merge_tree_attention(const lse_merge_tree_args* args, lse_merge_stream_t stream);
 

@@ -15,9 +15,10 @@ int check_kv_args(const lse_merge_kv_args& a, bool write);
 struct TreePlan {
     int G;             // query heads per KV head
     int rows;          // query rows of one (sequence, KV head): T * G
-    int shards;        // R, and one more for the drafts
+    int shards;        // R, and one more for the drafts: as many partials per row as any call of
+                       // these sizes has (more than 16 rows over a 16-bit cache: R, or none for R = 1)
     int64_t ws_l_off;  // workspace: partial o [B, T, Hq, shards, D] fp32, then lse [B, T, Hq, shards]
-    int64_t ws_bytes;  // 0 when one shard writes the result itself
+    int64_t ws_bytes;  // 0 for one shard without drafts, which writes the result itself
 };
 int tree_workspace(int B, int T, int Hq, int D, int R, bool drafts, TreePlan* plan);
 int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan);

@@ -11,7 +11,7 @@
 // The query rows of a (sequence, KV head) are the T * G pairs (token, head of
 // the group), row = t * G + g: all of them read the same keys.
 //
-// rows16 kernel: 16 rows per CTA, 4 warps, each with the key tiles w, w + 4,
+// rows16 kernel, up to 16 rows: one CTA per shard, 4 warps, each with the key tiles w, w + 4,
 // ... of the shard in a private ring filled by cp.async, an online softmax in
 // log2 units, mma.sync m16n8k16; the warps' states merge in shared memory.
 //   * 16-bit tiles: ldmatrix from XOR-swizzled rows (as decode_attention.cu).
@@ -536,7 +536,7 @@ struct Tiles8 {
 
 // One warp's share of a shard: tiles warp, warp + kRowWarps, ...
 template <typename Tiles, int D>
-__device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x, int row0, int rows, int warp,
+__device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x, int rows, int warp,
                                              int lane, unsigned char* ring, RowState<D>& w) {
     constexpr int TK = Tiles::TK, S = kRowStages;
     const uint32_t ring_u = smem_u32(ring);
@@ -550,14 +550,14 @@ __device__ __forceinline__ void attend_shard(const TreeParams& p, const Shard& x
         if (s < mine) Tiles::issue(p, x, x.lo + (warp + s * kRowWarps) * TK, ring_u + s * Tiles::kBytes, lane);
         cp_commit();
     }
-    const char* r0 = row0 + g < rows ? q_row(p, x.b, x.hk, row0 + g) : nullptr;
-    const char* r1 = row0 + g + 8 < rows ? q_row(p, x.b, x.hk, row0 + g + 8) : nullptr;
+    const char* r0 = g < rows ? q_row(p, x.b, x.hk, g) : nullptr;
+    const char* r1 = g + 8 < rows ? q_row(p, x.b, x.hk, g + 8) : nullptr;
     typename Tiles::Query q;
     Tiles::load_q(p, x, r0, r1, t, q);
     uint64_t word0 = ~0ull, word1 = ~0ull;
     if (x.drafts) {
-        word0 = r0 ? (uint64_t)p.tree[x.b * p.tree_b + (row0 + g) / p.G] : 0;
-        word1 = r1 ? (uint64_t)p.tree[x.b * p.tree_b + (row0 + g + 8) / p.G] : 0;
+        word0 = r0 ? (uint64_t)p.tree[x.b * p.tree_b + g / p.G] : 0;
+        word1 = r1 ? (uint64_t)p.tree[x.b * p.tree_b + (g + 8) / p.G] : 0;
     }
     for (int i = 0; i < mine; ++i) {
         if (i + S - 1 < mine)
@@ -607,8 +607,7 @@ __device__ __forceinline__ void store_state(float* st, int warp, int lane, const
         }
 }
 
-// grid (row tiles * shards, Hkv, B), row tiles fastest: the tiles of a shard
-// run at the same time and share its keys through L2
+// grid (shards, Hkv, B)
 template <typename T, int D, bool kFp8, bool kRows8, typename TOut>
 __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas) tree_rows16_kernel(const TreeParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -616,30 +615,29 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas) tree_rows16_kernel(c
     using Draft = Tiles16<T, D, kRows8>;
     constexpr int kRing = kRowStages * (Cache::kBytes > Draft::kBytes ? Cache::kBytes : Draft::kBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.x / p.row_tiles, row0 = (blockIdx.x - r * p.row_tiles) * 16;
     const int rows = p.T * p.G;
     pdl_wait();
     pdl_release();
-    Shard x = shard_of(p, r, blockIdx.y, blockIdx.z);
-    if (row0 >= x.live * p.G) x.hi = x.lo;   // dead rows only
+    Shard x = shard_of(p, blockIdx.x, blockIdx.y, blockIdx.z);
+    if (x.live == 0) x.hi = x.lo;   // dead rows only
     RowState<D> w;
     unsigned char* ring = smem + warp * kRing;
     float* st = reinterpret_cast<float*>(smem);
     if (kFp8 && !x.drafts) {
-        attend_shard<Cache, D>(p, x, row0, rows, warp, lane, ring, w);
+        attend_shard<Cache, D>(p, x, rows, warp, lane, ring, w);
         __syncthreads();
         store_state<Cache, D>(st, warp, lane, w);
     } else {
-        attend_shard<Draft, D>(p, x, row0, rows, warp, lane, ring, w);
+        attend_shard<Draft, D>(p, x, rows, warp, lane, ring, w);
         __syncthreads();
         store_state<Draft, D>(st, warp, lane, w);
     }
     __syncthreads();
     const float* st_o = st + 2 * kRowWarps * 16;
     for (int idx = threadIdx.x; idx < 16 * D; idx += kRowWarps * 32) {
-        const int i = idx / D, d = idx - i * D, row = row0 + i;
-        if (row >= rows) break;
-        const int t = row / p.G;
+        const int i = idx / D, d = idx - i * D;   // row i
+        if (i >= rows) break;
+        const int t = i / p.G;
         float M = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kRowWarps; ++v) M = fmaxf(M, st[v * 16 + i]);
@@ -657,7 +655,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas) tree_rows16_kernel(c
         const bool any = den != 0.f;   // NaN where a score was
         const float o = any ? num / den : 0.f;
         const float lse = any ? (M + log2f(den)) * kLn2 : -INFINITY;
-        const int64_t at = ((int64_t)x.b * p.T + t) * p.Hq + x.hk * p.G + (row - t * p.G);
+        const int64_t at = ((int64_t)x.b * p.T + t) * p.Hq + x.hk * p.G + (i - t * p.G);
         if (p.po) {
             p.po[(at * p.shards + x.r) * D + d] = o;
             if (d == 0) p.pl[at * p.shards + x.r] = lse;
@@ -865,7 +863,6 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
     p.fold = wide && !fp8 && drafts;
     p.join = wide && fp8 && drafts && a.R == 1;
     p.shards = p.fold ? a.R : p.join ? 1 : pl.shards;
-    p.row_tiles = (pl.rows + 15) / 16;
     p.scale_log2 = a.scale * kLog2e;
     if (p.shards > 1 || p.join) {
         p.po = static_cast<float*>(a.workspace);
@@ -897,14 +894,14 @@ int launch_tree(const lse_merge_tree_args* args, cudaStream_t stream) {
                                                       : pick_tree<__nv_bfloat16>(a.D, fp8, pl.rows <= 8, a.out_dtype);
         e = allow_smem((const void*)k.fn, k.smem);
         if (e == cudaSuccess) {
-            cfg.gridDim = dim3((unsigned)(p.row_tiles * p.shards), (unsigned)a.Hkv, (unsigned)a.B);
+            cfg.gridDim = dim3((unsigned)p.shards, (unsigned)a.Hkv, (unsigned)a.B);
             cfg.blockDim = dim3(kRowWarps * 32);
             cfg.dynamicSmemBytes = (size_t)k.smem;
             e = cudaLaunchKernelEx(&cfg, k.fn, p);
         }
     }
     if (e == cudaSuccess && p.shards > 1) {
-        // a block per row where a group's loads would come in more than one batch of 4
+        // a block per row, whose groups share the shards, for more than 4 of them
         const bool spread = p.shards > 4;
         const uint32_t rows = (uint32_t)a.B * a.T * a.Hq, per = spread ? 1u : 128u / (uint32_t)(a.D / 4);
         cfg.gridDim = dim3((rows + per - 1) / per);

@@ -22,7 +22,8 @@ struct TreeParams {
     int64_t kd_b, kd_h, kd_t, vd_b, vd_h, vd_t;
     int64_t ks_b, ks_h, ks_l, vs_b, vs_h, vs_l;     // element strides
     int64_t tree_b;
-    int T, Hq, G, L, R, shards, row_tiles;
+    int T, Hq, G, L, R, shards;
+    int row_tiles;      // wide kernel: of 256 rows
     int r0;             // shard of the launch's first block
     int fold;           // the last cached shard has the drafts too
     int join;           // po and pl hold one shard's partials, which the launch merges with its own shard
