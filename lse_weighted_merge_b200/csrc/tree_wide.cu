@@ -809,17 +809,17 @@ __device__ __forceinline__ void softmax_half(Scores x, uint32_t tO, uint32_t o_d
             }
         }
         if (x.v4 || !__all_sync(kFull, st.gain == g)) {
-            const float h = st.gain == 0.f ? 1.f : g * pow2_inverse(st.gain);
-            const float was = st.peak * down * h;   // what O's largest part is at gain g
+            const float old = st.gain == 0.f ? g : st.gain;
+            const float was = st.peak * down * (g * pow2_inverse(old));   // what O's largest part is at gain g
             float more = 1.f;
             if (values.y == (float)kZeros) {
                 most = 0.f;
             } else if (was <= kMostPeak) {
                 const float row = fmaxf(was, most);
-                if (x.v4 && row < 8.f && row > 0.f)
-                    more = fminf(512.f * pow2_inverse(pow2_below(row)), 1.3292280e36f * pow2_inverse(g));
-                down *= h * more;
+                if (x.v4 && row < 8.f && row > 0.f)   // (at most 2^80, and the gain at most 2^120)
+                    more = fminf(512.f * pow2_inverse(pow2_below(row)), fminf(1.2089258e24f, 1.3292280e36f * values.x));
                 st.gain = g * more;
+                down *= st.gain * pow2_inverse(old);
             } else {   // next to nothing beside what O has: left out
                 more = 0.f;
             }

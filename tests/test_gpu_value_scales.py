@@ -159,6 +159,34 @@ def test_a_sink_of_zeros(T, ahead, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS8)
+@pytest.mark.parametrize("ahead", [60, 100, 118, 140, 300])
+@pytest.mark.parametrize("exponent", [-20, 0, 20])
+@pytest.mark.parametrize("T", ROWS)
+def test_a_sink_of_zeros_over_values_of_all_sizes(T, exponent, ahead, kind):
+    """The same with weights of the others near fp32's smallest or below, and values whose
+    scales lie far apart: next to nothing, but finite."""
+    for at in (0, 130, 639):
+        c = case(kind, T, 640, 128, exponent)
+        g = torch.Generator(device="cuda").manual_seed(ahead)
+        s = c.scales["v_scale"]
+        s *= torch.exp2(torch.randint(-15, 16, s.shape, generator=g, device="cuda").float())
+        c.q[..., 0] = 16.0
+        c.k.view(torch.uint8)[..., 0] = 0
+        c.k.view(torch.uint8)[:, :, at] = 0
+        c.k[:, :, at, 0] = torch.tensor(1.0, device="cuda").to(c.k.dtype)
+        c.scales["k_scale"][:, :, at] = ahead * math.log(2) * math.sqrt(128) / 16
+        zero_values(c, at)
+        ref = attention(c.q, c.whole("k"), c.whole("v"))
+        for splits in (1, 3):
+            out, lse = c.run(drafts=False, splits=splits, out_dtype=torch.float32)
+            assert bool(torch.isfinite(out).all()), f"at {at}, {splits} shards"
+            # weights below 2^-100 may be lost, those of the wider kernel below 2^-32
+            floor = 640 * (2.0 ** -100 if T * 4 <= 16 else 2.0 ** -31) * float(c.whole("v").abs().max())
+            assert bool(((out.double() - ref[0]).abs() <= 2.0 ** -9 * ref[2] + floor).all())
+            assert float((lse.double() - ref[1]).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("kind", KINDS8)
 def test_values_that_are_all_zeros(kind):
     for T in ROWS:
         c = case(kind, T, 300, 64, -20)
