@@ -37,7 +37,8 @@
 // there, whatever it is, meets a weight of 0.
 //
 // Measured on B200, 16 trees of 64 drafts, 32 heads over 8, D = 128, 8192 e4m3
-// tokens: 224 us, 612 TFLOP/s (the rows16 kernel: 913); 16 trees of 16 over 4096
+// tokens: 226 us, 609 TFLOP/s (the rows16 kernel: 913; scales that are no powers of two:
+// 337; a row of zeros of another size every 50 tokens: 267); 16 trees of 16 over 4096
 // bf16 tokens: 58 to 66 us, 4.2 to 4.6 TB/s (186).  The exponentials (16 per clock and SM)
 // and the tensor cores bound a tile of 128 rows and 128 keys at 1024 clocks alike;
 // a softmax warp takes about 2500 clocks for a half, of which the exponentials are
