@@ -328,7 +328,8 @@ int lse_merge_kv_dequantize(const lse_merge_kv_args* args, lse_merge_stream_t st
  *
  *   q            [B, T, Hq, D] of dtype; k_draft, v_draft [B, Hkv, T, D] of dtype
  *   k, v         the cache [B, Hkv, L, D], of dtype (cache_dtype == dtype) or
- *                LSE_MERGE_E4M3 with k_scale and v_scale [B, Hkv, L], positive
+ *                LSE_MERGE_E4M3 with k_scale and v_scale [B, Hkv, L], positive (0 stands
+ *                for a key or value of zeros); v_scale within 2^70 of each other
  *   tree         int64 [B, T] (row stride tree_b; 0 = the same tree for all)
  *   out_o        dense [B, T, Hq, D] of out_dtype; out_lse dense [B, T, Hq] fp32
  *   dtype        LSE_MERGE_BF16 or LSE_MERGE_F16;  1 <= T <= 64;  D 64 or 128;

@@ -93,7 +93,8 @@ def decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, *, kv_len=None, 
 
     q [B, Hq, D] (bfloat16 or float16); k_cache, v_cache float8_e4m3fn [B, Hkv,
     L, D] with k_scale, v_scale float32 [B, Hkv, L], as kv_quantize_ leaves
-    them (any positive scales do); Hq a multiple of Hkv, at most 16 times; D 64
+    them (any positive scales do, the values' within 2^70 of each other; 0 stands
+    for a key or value of zeros); Hq a multiple of Hkv, at most 16 times; D 64
     or 128; kv_len an optional int32 tensor [B].  The keys are cut into
     ``splits`` shards whose partials are merged by weight (default: enough to
     fill the GPU).  L is 1 or more (an empty cache is kv_len 0).  Returns (out

@@ -209,3 +209,17 @@ def test_a_written_prompt_with_padding(kind):
     lm.kv_quantize_(c.k, c.v, c.scales["k_scale"], c.scales["v_scale"], k, v,
                     torch.zeros(B, dtype=torch.int32, device="cuda"))
     check_weighted(c)
+
+
+@pytest.mark.parametrize("kind", KINDS8)
+@pytest.mark.parametrize("T", ROWS)
+def test_rows_that_were_never_written(T, kind):
+    """Zeros with scale 0, as a cache of zeros starts out: keys of score 0, values of 0."""
+    for where in ([0], list(range(100, 300)), list(range(640)), [5, 639]):
+        c = case(kind, T, 640, 64, -12)
+        for x in (c.k, c.v):
+            x.view(torch.uint8)[:, :, where] = 0
+        for s in c.scales.values():
+            s[:, :, where] = 0
+        for splits in (1, 3, None):
+            check_weighted(c, f"{len(where)} rows, {splits} shards", splits=splits)
