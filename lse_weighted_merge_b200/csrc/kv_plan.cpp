@@ -219,7 +219,8 @@ int make_tree_plan(const lse_merge_tree_args& a, TreePlan* plan) {
     if (a.L > INT32_MAX - 1024) return LSE_MERGE_EDIMS;
     // row indexes of the merge fit 30 bits
     if ((i128)a.B * a.T * a.Hq > ((i128)1 << 30)) return LSE_MERGE_EDIMS;
-    if (!(a.scale == a.scale) || a.scale > 3.0e38f || a.scale < -3.0e38f) return LSE_MERGE_EDIMS;
+    // times log2(e) it stays finite (NaN fails too)
+    if (!(a.scale <= 2.3e38f && a.scale >= -2.3e38f)) return LSE_MERGE_EDIMS;
     if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out_o, 16) ||
         !aligned(a.out_lse, 4) || !aligned(a.kv_len, 4) || !aligned(a.draft_len, 4))
         return LSE_MERGE_EALIGN;

@@ -16,3 +16,12 @@ def test_key_indexes_that_would_pass_32_bits(L, T, cache):
     rc = tree(L=L, T=T, c=(128, 64, 0), s=(2, 1, 0), d=(T * 128, T * 64, 64), qs=(T * 512, 512, 64), tree_b=T,
               **cache, **far)
     assert rc == nat.EDIMS, nat.strerror(rc)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("scale", [2.5e38, -2.9e38, float("nan"), float("-inf")])
+def test_scales_that_overflow_in_powers_of_two(scale, T):
+    """The kernels work in powers of two: scale * log2(e) has to be finite."""
+    far = {n: a + (1 << 44) for n, a in A.items() if n in ("out", "lse", "ws")}
+    rc = tree(T=T, scale=scale, d=(T * 128, T * 64, 64), qs=(T * 512, 512, 64), tree_b=T, **far)
+    assert rc == nat.EDIMS, nat.strerror(rc)
