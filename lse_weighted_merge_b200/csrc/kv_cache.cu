@@ -12,7 +12,7 @@
 // so e = exponent(a) - 8, and one more where the mantissa is above 1.75.
 //
 // Both kernels are bound by memory, with 16 elements of a row per lane.  Writing
-// 16 x 4096 tokens of 8 heads, D = 128, bf16, takes 66 to 71 us by box (5.8 to 6.1
+// 16 x 4096 tokens of 8 heads, D = 128, bf16, takes 66 to 71 us by GPU (5.8 to 6.1
 // TB/s, 88 to 92 % of the measured copy rate).  With tests for infinities on every
 // element it was bound by the compares (98 us): the maximum is taken over the
 // magnitudes' bits, two 16-bit ones per instruction, and shows infinities and NaN
