@@ -33,13 +33,13 @@
 //   * Up to 8 rows (a decode step, mostly) leave the products' rows 8 to 15 empty;
 //     nothing but the products is then done for them.
 // Measured on B200, 64 sequences of 4096 e4m3 tokens, 32 heads over 8, D = 128:
-// 98 us, 5.7 TB/s, 87 % of the measured copy rate (95 us where the keys of the call
-// before are partly in L2 still).  Bound by the instructions per key (codes to f16,
-// products that use 4 of 16 rows) and their latencies: two warps per scheduler use 37 %
-// of the issue slots.  The gains cost 1 us of that.  Earlier forms, on a slower GPU
-// where this took 103: tests in full tiles too 106, three CTAs per SM with two stages
-// each 112 (512 CTAs leave a tail), scaling o in every tile and all rows' softmax 119.
-// One sequence, 16 shards: 10.2 to 13 us by machine with the merge, latency.
+// 98 to 103 us by GPU, 5.4 to 5.7 TB/s, 82 to 87 % of the measured copy rate (95 us
+// where the keys of the call before are partly in L2 still).  Bound by the instructions
+// per key (codes to f16, products that use 4 of 16 rows) and their latencies: two warps
+// per scheduler use 37 % of the issue slots.  The gains cost 1 us of that.  Other forms:
+// tests in full tiles too 106, three CTAs per SM with two stages each 112 (512 CTAs leave
+// a tail), scaling o in every tile and all rows' softmax 119.  One sequence, 16 shards:
+// 10.2 to 13 us by machine with the merge, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

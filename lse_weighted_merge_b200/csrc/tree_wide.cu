@@ -36,17 +36,17 @@
 // of the unrounded ones.  Keys past the shard's end are zeros, so that no value
 // there, whatever it is, meets a weight of 0.
 //
-// Measured on B200, 16 trees of 64 drafts, 32 heads over 8, D = 128, 8192 e4m3
-// tokens: 226 us, 609 TFLOP/s (the rows16 kernel: 913; scales that are no powers of two:
-// 337; a row of zeros of another size every 50 tokens: 267); 16 trees of 16 over 4096
-// bf16 tokens: 58 to 66 us, 4.2 to 4.6 TB/s (186).  The exponentials (16 per clock and SM)
-// and the tensor cores bound a tile of 128 rows and 128 keys at 1024 clocks alike;
-// a softmax warp takes about 2500 clocks for a half, of which the exponentials are
-// 512: its own chain of barrier, TMEM load, weights, TMEM store and barrier, not a
-// unit, is what is left (no unit is busy more than 30 % of the time).  Taking the
-// exponentials out saves 19 %, the products 7 %, the conversion 5 %.  Two threads
-// per row (16 softmax warps) gave 236 us, halves of 128 keys with one buffer 207
-// instead of 199 for the cached part, a prefetch into L2 four tiles ahead nothing.
+// Measured on B200, 16 trees of 64 drafts, 32 heads over 8, D = 128, 8192 e4m3 tokens:
+// 226 to 228 us, 603 to 609 TFLOP/s (the rows16 kernel: 913; scales that are no powers
+// of two: 337; a row of zeros of another size every 50 tokens: 267); 16 trees of 16
+// over 4096 bf16 tokens: 58 to 66 us, 4.2 to 4.6 TB/s (186). The exponentials (16 per
+// clock and SM) and the tensor cores bound a tile of 128 rows and 128 keys at 1024
+// clocks alike; a softmax warp takes about 2500 clocks for a half, of which the
+// exponentials are 512: its own chain of barrier, TMEM load, weights, TMEM store and
+// barrier, not a unit, is what is left (no unit is busy more than 30 % of the time).
+// Taking the exponentials out saves 19 %, the products 7 %, the conversion 5 %. Two
+// threads per row (16 softmax warps) gave 236 us, halves of 128 keys with one buffer
+// 207 instead of 199 for the cached part, a prefetch into L2 four tiles ahead nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
